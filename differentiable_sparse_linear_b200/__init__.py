@@ -9,6 +9,10 @@ Functions keep the C names (``sla_spmv``, ``sla_pcg_solve``, ``sla_pcg_adjoint``
 "torch-sla: Differentiable Sparse Linear Algebra with Adjoint Solvers and Sparse Tensor
 Parallelism for PyTorch", Methodology §2 (Linear Systems): one solve with A^T = A,
 dL/db = lambda, dL/dA_ij = -lambda_i x_j on A's pattern; only x is saved for backward.
+
+The sequence operators (gated linear recurrence, routing of tokens to experts) are in
+``sequence`` and exported here: ``recurrence``, ``sla_route_sort``, ``route_dispatch``,
+``route_combine`` and the sla_recur_* / sla_route_* calls under them.
 """
 from __future__ import annotations
 
@@ -24,6 +28,9 @@ from . import _lib
 from ._lib import (SLA_BREAKDOWN, SLA_ERR_CUDA, SLA_ERR_INVALID_ARG, SLA_ERR_INVALID_CSR,
                    SLA_ERR_OOM, SLA_ERR_UNSUPPORTED, SLA_F32, SLA_F64, SLA_NOT_CONVERGED,
                    SLA_SPD, SLA_STATIC_VALUES, SLA_SUCCESS, SLA_VALIDATE)
+from .sequence import (GATES, Route, recurrence, route_combine, route_dispatch, sla_recur_adjoint,
+                       sla_recur_solve, sla_recur_step, sla_route_combine, sla_route_combine_adjoint,
+                       sla_route_dispatch, sla_route_dispatch_adjoint, sla_route_sort)
 
 __all__ = [
     "SlaError", "Matrix", "Preconditioner", "PcgInfo", "PcgInfoList", "lib",
@@ -33,7 +40,9 @@ __all__ = [
     "sla_pcg_solve_batched_noalloc", "sla_list_kernel_ms", "sla_eigen_grad", "sla_csr_add_diagonal", "sla_nonlinear_adjoint",
     "sla_vec_dot", "sla_pcg_update", "sla_pcg_direction", "sla_vec_gather", "sla_vec_scatter_add",
     "sla_workspace_bytes", "sla_pcg_kernel_times", "sla_pcg_phase_times", "solve",
-    "ENGINES",
+    "ENGINES", "GATES", "Route", "recurrence", "route_dispatch", "route_combine",
+    "sla_recur_solve", "sla_recur_adjoint", "sla_recur_step", "sla_route_sort", "sla_route_dispatch",
+    "sla_route_combine", "sla_route_dispatch_adjoint", "sla_route_combine_adjoint",
 ]
 
 

@@ -17,9 +17,12 @@ SLA_ERR_OOM = -4
 SLA_ERR_UNSUPPORTED = -5
 SLA_F32 = 0
 SLA_F64 = 1
+SLA_BF16 = 2
+SLA_F16 = 3
 SLA_SPD = 1
 SLA_VALIDATE = 2
 SLA_STATIC_VALUES = 4
+SLA_FILL_REST = 1
 SLA_ENGINE_AUTO = 0
 SLA_ENGINE_GRAPH = 1
 SLA_ENGINE_PERSISTENT = 2
@@ -38,6 +41,7 @@ class sla_pcg_info(C.Structure):
 
 _vp = C.c_void_p
 _st = C.c_int32
+_i32, _i64, _u32, _sz = C.c_int32, C.c_int64, C.c_uint32, C.c_size_t
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -76,6 +80,22 @@ SIGNATURES = {
     "sla_pcg_direction": (_st, [C.c_int32, C.c_int64, C.c_double, _vp, _vp, _vp]),
     "sla_vec_gather": (_st, [C.c_int32, C.c_int64, _vp, _vp, _vp, _vp]),
     "sla_vec_scatter_add": (_st, [C.c_int32, C.c_int64, _vp, _vp, _vp, _vp]),
+    "sla_recur_workspace_bytes": (_sz, [_i32, _i64, _i64]),
+    "sla_recur_solve": (_st, [_i32, _i32, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp,
+                              _u32, _vp, _sz, _vp]),
+    "sla_recur_adjoint": (_st, [_i32, _i32, _i64, _i64, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
+                                _i64, _vp, _vp, _i64, _vp, _i64, _vp, _u32, _vp, _sz, _vp]),
+    "sla_recur_step": (_st, [_i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64,
+                             _u32, _vp]),
+    "sla_route_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "sla_route_sort": (_st, [_i64, _i32, _i32, _i32, _vp, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sla_route_dispatch": (_st, [_i32, _i64, _i32, _i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64,
+                                 _u32, _vp]),
+    "sla_route_combine": (_st, [_i32, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "sla_route_dispatch_adjoint": (_st, [_i32, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp,
+                                         _i64, _vp, _vp]),
+    "sla_route_combine_adjoint": (_st, [_i32, _i64, _i32, _i32, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp,
+                                        _i64, _vp, _i64, _vp, _u32, _vp]),
     "sla_list_kernel_ms": (_st, [_vp, C.POINTER(C.c_double)]),
     "sla_pcg_solve_batched_noalloc": (_st, [_vp, _vp, _vp, _vp, C.POINTER(sla_pcg_opts),
                                             C.POINTER(sla_pcg_info), _vp]),

@@ -73,7 +73,9 @@ typedef int32_t sla_status;
 #define SLA_ERR_OOM (-4)          /* device or host allocation failed                   */
 #define SLA_ERR_UNSUPPORTED (-5)  /* valid request outside what this build implements   */
 
-typedef enum { SLA_F32 = 0, SLA_F64 = 1 } sla_dtype;
+/* Value types.  Matrices and the solver's vectors are SLA_F32 or SLA_F64; the rows of the
+ * sequence operators (sla_recur_*, sla_route_*) may also be SLA_BF16 or SLA_F16. */
+typedef enum { SLA_F32 = 0, SLA_F64 = 1, SLA_BF16 = 2, SLA_F16 = 3 } sla_dtype;
 
 /* Flags for sla_csr_create*. */
 #define SLA_SPD 1u        /* caller asserts A is symmetric positive definite (needed by PCG) */
@@ -344,6 +346,135 @@ SLA_API sla_status sla_pcg_solve_batched_noalloc(const sla_csr *A, const sla_pre
                                                  const void *d_B, void *d_X,
                                                  const sla_pcg_opts *opts, sla_pcg_info *h_info,
                                                  void *stream);
+
+/* ---------------------------------------------------------------- sequence operators
+ * Two sparse matrices that a sequence model applies to its tokens, each with its transpose and
+ * the gradient on its stored entries, as the calls above have them for SPD systems:
+ *
+ *   the gated linear recurrence   h_t = a_t h_{t-1} + w_t b_t per sequence and channel, which is
+ *       the solve L h = w b with L unit lower bidiagonal (-a_t below the diagonal); backward the
+ *       solve with L^T and the gradient of the subdiagonal's entries;
+ *   routing                       R (tokens x slots) with one entry per used slot: tokens sorted
+ *       by the expert they are sent to, the products R^T X (rows to the experts) and R Y (the
+ *       weighted sum back), and the gradient of R's entries.
+ *
+ * Conventions of these calls, beyond the general ones
+ *   - Rows are [n_tokens][n_chan], channels contiguous, with a row stride `ld*` in elements
+ *     (ld >= n_chan; an input's ld may be 0, one row for every token).  Values are SLA_F32,
+ *     SLA_F64, SLA_BF16 or SLA_F16; arithmetic, states, weights and their gradients are fp32
+ *     (fp64 with SLA_F64 rows), and every row value is rounded once, when it is written.
+ *     Row pointers need the alignment of their type only.
+ *   - Packed sequences: sequence s owns rows [d_seq_off[s], d_seq_off[s+1]) of the packed rows
+ *     (device int32, n_seq + 1 entries, ascending, within [0, n_tokens]; empty sequences
+ *     allowed).  NULL: n_seq sequences of n_tokens / n_seq rows each.  Rows outside every
+ *     sequence are not read; they are left as they were, or set to zero with SLA_FILL_REST.
+ *   - None of the calls allocates, synchronises or keeps anything: scratch memory is the
+ *     caller's d_work (16-byte aligned; its contents before and after are unspecified).  Calls
+ *     that may run at the same time, replays of captured graphs among them, need a d_work
+ *     each.  All calls can be captured into a CUDA graph; offsets, indices and plans are read
+ *     when the work runs.
+ *   - Results do not depend on the order in which blocks run: the same inputs give the same bits.
+ *   - Outputs must not overlap inputs or each other unless a call says so. */
+#define SLA_FILL_REST 1u /* rows (slots) that belong to nothing are written as zeros */
+
+/* What the coefficients d_a hold (z is the stored value). */
+typedef enum {
+    SLA_GATE_VALUE = 0,   /* a = z,          input weight w = 1                                */
+    SLA_GATE_EXP = 1,     /* a = exp(z),     w = 1 (z = log of the decay)                      */
+    SLA_GATE_SIGMOID = 2  /* a = sigmoid(z), w = 1 - a (a convex combination of state and input) */
+} sla_gate;
+
+/* Bytes of d_work that sla_recur_solve and sla_recur_adjoint need (0: d_work may be NULL). */
+SLA_API size_t sla_recur_workspace_bytes(int32_t dtype, int64_t n_tokens, int64_t n_chan);
+
+/* h_t = a_t h_{t-1} + w_t b_t over every sequence, from d_h0 (n_seq x n_chan, fp32 or fp64;
+ * NULL: zero state, and then the coefficient of a sequence's first row is not used).  d_h gets
+ * the rows; d_h_last (n_seq x n_chan, fp32/fp64, may be NULL) the unrounded last states (an empty
+ * sequence's is its first one).  flags: 0 or SLA_FILL_REST. */
+SLA_API sla_status sla_recur_solve(int32_t dtype, int32_t gate, int64_t n_tokens, int64_t n_chan,
+                                   int32_t n_seq, const int32_t *d_seq_off, const void *d_a,
+                                   int64_t lda, const void *d_b, int64_t ldb, const void *d_h0,
+                                   void *d_h, int64_t ldh, void *d_h_last, uint32_t flags,
+                                   void *d_work, size_t work_bytes, void *stream);
+
+/* The adjoint: with g_t = dL/dh_t (d_dh, NULL: zero) and dL/d(last state) (d_dh_last, NULL: zero)
+ *   lambda_t = g_t + a_{t+1} lambda_{t+1}   (at a sequence's last row: g_t + d_dh_last)
+ *   db_t = w_t lambda_t,   dz_t = lambda_t da_t/dz (h_{t-1}, less b_t for the sigmoid gate),
+ *   dh0 = a_first lambda_first.
+ * d_h are the rows sla_recur_solve wrote (in their row type), d_b its inputs (read for the
+ * sigmoid gate with d_dz only, NULL otherwise).  d_dz (dL/d of the stored coefficients) or d_db may
+ * be NULL to skip them; d_dh0 (n_seq x n_chan, fp32/fp64) may be NULL and needs d_h0. */
+SLA_API sla_status sla_recur_adjoint(int32_t dtype, int32_t gate, int64_t n_tokens, int64_t n_chan,
+                                     int32_t n_seq, const int32_t *d_seq_off, const void *d_a,
+                                     int64_t lda, const void *d_b, int64_t ldb, const void *d_h,
+                                     int64_t ldh, const void *d_h0, const void *d_dh, int64_t lddh,
+                                     const void *d_dh_last, void *d_dz, int64_t lddz, void *d_db,
+                                     int64_t lddb, void *d_dh0, uint32_t flags, void *d_work,
+                                     size_t work_bytes, void *stream);
+
+/* One row for each of n_rows sequences of a serving batch, on states kept in a pool: with
+ * i = d_index[r] (NULL: r), d_state[i] = a_r d_state[i] + w_r b_r in place, and d_h[r] is the new
+ * state, rounded.  d_state: n_slots rows of n_chan fp32 (fp64) values, stride ldstate.  Rows whose
+ * index is outside [0, n_slots) are padding: they change no state, and their d_h is left as it
+ * was (zeros with SLA_FILL_REST).  The other indices of one call must be distinct. */
+SLA_API sla_status sla_recur_step(int32_t dtype, int32_t gate, int64_t n_rows, int64_t n_chan,
+                                  int64_t n_slots, const void *d_a, int64_t lda, const void *d_b,
+                                  int64_t ldb, void *d_state, int64_t ldstate,
+                                  const int32_t *d_index, void *d_h, int64_t ldh, uint32_t flags,
+                                  void *stream);
+
+/* The routing plan.  d_expert: n_tokens x top_k expert ids (int32, or int64 with id_bytes = 8),
+ * row-major; entry (t, j) is number t * top_k + j.  Ids outside [0, n_experts) are dropped; the same
+ * expert twice in a row of d_expert takes two slots.  Entries are sorted by expert, in the order of
+ * their numbers within one expert, and every expert's slots are padded to a multiple of `align`:
+ *   d_offsets (n_experts + 1)  first slot of each expert; the last is the number of slots in use
+ *   d_counts  (n_experts)      entries of each expert (the rest of its slots is padding)
+ *   d_entry   (n_slots)        entry number in a slot; -1 in padding and behind the slots in use
+ *   d_slot    (n_tokens x top_k) slot of each entry, -1 if it was dropped
+ * n_slots >= n_tokens * top_k + n_experts * (align - 1), and below 2^31.  1 <= n_experts <= 4096
+ * (SLA_ERR_UNSUPPORTED above), top_k >= 1, align >= 1. */
+SLA_API size_t sla_route_workspace_bytes(int64_t n_tokens, int32_t top_k, int32_t n_experts);
+SLA_API sla_status sla_route_sort(int64_t n_tokens, int32_t top_k, int32_t n_experts, int32_t align,
+                                  const void *d_expert, int32_t id_bytes, int64_t n_slots,
+                                  int32_t *d_offsets, int32_t *d_counts, int32_t *d_entry,
+                                  int32_t *d_slot, void *d_work, size_t work_bytes, void *stream);
+
+/* Products with the routing matrix R, whose entry (t, slot[t][j]) is d_weight[t][j] (fp32; fp64
+ * with SLA_F64 rows; NULL: 1).  d_offsets, d_counts, d_slot are the plan's, unchanged.  Token side
+ * n_tokens rows, slot side n_slots rows.
+ *
+ * Dispatch, xs = R^T x: a used slot gets its token's row times its weight, a padding slot zeros;
+ * slots at and behind d_offsets[n_experts] are left as they were (zeros with SLA_FILL_REST). */
+SLA_API sla_status sla_route_dispatch(int32_t dtype, int64_t n_tokens, int32_t top_k, int32_t n_experts,
+                                      int64_t n_slots, int64_t n_chan, const void *d_x, int64_t ldx,
+                                      const int32_t *d_offsets, const int32_t *d_counts,
+                                      const int32_t *d_slot, const void *d_weight, void *d_xs,
+                                      int64_t ldxs, uint32_t flags, void *stream);
+
+/* Combine, y = R ys: every token's sum over its slots in the order of j, summed in fp32 (fp64);
+ * a token without slots gets zeros.  Rows of padding slots are not read. */
+SLA_API sla_status sla_route_combine(int32_t dtype, int64_t n_tokens, int32_t top_k, int64_t n_slots,
+                                     int64_t n_chan, const void *d_ys, int64_t ldys,
+                                     const int32_t *d_slot, const void *d_weight, void *d_y,
+                                     int64_t ldy, void *stream);
+
+/* Adjoint of dispatch: dx = R dxs and, where d_dweight is not NULL, the gradient on R's pattern
+ * d_dweight[t][j] = x_t . dxs_slot (0 for dropped entries); d_x is read for d_dweight only. */
+SLA_API sla_status sla_route_dispatch_adjoint(int32_t dtype, int64_t n_tokens, int32_t top_k,
+                                              int64_t n_slots, int64_t n_chan, const void *d_dxs,
+                                              int64_t lddxs, const int32_t *d_slot,
+                                              const void *d_weight, const void *d_x, int64_t ldx,
+                                              void *d_dx, int64_t lddx, void *d_dweight, void *stream);
+
+/* Adjoint of combine: dys = R^T dy (padding, rest and flags as in dispatch) and, where d_dweight is
+ * not NULL, d_dweight[t][j] = dy_t . ys_slot; d_ys is read for d_dweight only. */
+SLA_API sla_status sla_route_combine_adjoint(int32_t dtype, int64_t n_tokens, int32_t top_k,
+                                             int32_t n_experts, int64_t n_slots, int64_t n_chan,
+                                             const void *d_dy, int64_t lddy, const int32_t *d_offsets,
+                                             const int32_t *d_counts, const int32_t *d_slot,
+                                             const void *d_weight, const void *d_ys, int64_t ldys,
+                                             void *d_dys, int64_t lddys, void *d_dweight,
+                                             uint32_t flags, void *stream);
 
 /* Per-kernel device time of one PCG iteration (metrics).  On the workspace of the
  * (A, M, nrhs, vector_f64) solver -- normally right after a solve, so it holds that solve's vectors --
