@@ -1,113 +1,12 @@
-// Gated linear recurrence h_t = a_t h_{t-1} + w_t b_t over packed sequences: the solve with a unit
-// lower bidiagonal matrix, its adjoint (the solve with the transpose, and the gradient on the
-// subdiagonal), and the single-row step on a pool of states.
-#include <cuda_runtime.h>
-
-#include <algorithm>
-
-#include "seq_rows.cuh"
+// Gated linear recurrence h_t = a_t h_{t-1} + w_t b_t over packed sequences: the entry points of the solve
+// with a unit lower bidiagonal matrix and of its adjoint (recur_core.cuh), and the single-row step
+// on a pool of states.
+#include "recur_core.cuh"
 
 namespace sla {
 namespace {
 
 constexpr int RT = 128;
-
-struct SeqBounds {
-    const int32_t *off;   // NULL: equal lengths
-    int64_t n_tokens;
-    int32_t n_seq;
-    // Offsets are read from the device and clamped, so that no offset leads outside the rows.
-    __device__ __forceinline__ int64_t at(int64_t s) const
-    {
-        if (!off)
-            return n_tokens / n_seq * s;
-        const int64_t v = off[s];
-        return v < 0 ? 0 : v > n_tokens ? n_tokens : v;
-    }
-};
-
-template <typename S, int GATE>
-__global__ void __launch_bounds__(RT) k_recur_solve(SeqBounds q, int64_t n_chan, const S *a, int64_t lda, const S *b,
-                                                    int64_t ldb, const typename RowType<S>::A *h0, S *h, int64_t ldh,
-                                                    typename RowType<S>::A *last)
-{
-    using R = RowType<S>;
-    using A = typename R::A;
-    const int64_t c = (int64_t)blockIdx.x * RT + threadIdx.x;
-    if (c >= n_chan)
-        return;
-    for (int64_t s = blockIdx.y; s < q.n_seq; s += gridDim.y) {
-        const int64_t t0 = q.at(s), t1 = q.at(s + 1);
-        A v = h0 ? h0[s * n_chan + c] : A(0);
-        for (int64_t t = t0; t < t1; ++t) {
-            A ca, w;
-            gate_of<GATE>(R::up(a[t * lda + c]), ca, w);
-            const A u = w * R::up(b[t * ldb + c]);
-            v = (t == t0 && !h0) ? u : fma_of(ca, v, u);
-            h[t * ldh + c] = R::down(v);
-        }
-        if (last)
-            last[s * n_chan + c] = v;
-    }
-}
-
-template <typename S, int GATE>
-__global__ void __launch_bounds__(RT)
-    k_recur_adjoint(SeqBounds q, int64_t n_chan, const S *a, int64_t lda, const S *b, int64_t ldb, const S *h,
-                    int64_t ldh, const typename RowType<S>::A *h0, const S *dh, int64_t lddh,
-                    const typename RowType<S>::A *dlast, S *dz, int64_t lddz, S *db, int64_t lddb,
-                    typename RowType<S>::A *dh0)
-{
-    using R = RowType<S>;
-    using A = typename R::A;
-    const int64_t c = (int64_t)blockIdx.x * RT + threadIdx.x;
-    if (c >= n_chan)
-        return;
-    for (int64_t s = blockIdx.y; s < q.n_seq; s += gridDim.y) {
-        const int64_t t0 = q.at(s), t1 = q.at(s + 1);
-        // lambda_t = g_t + a_{t+1} lambda_{t+1} by one fused multiply-add, written out so that every
-        // variant of the loop rounds alike
-        A next = A(1), lam = dlast ? dlast[s * n_chan + c] : A(0);
-        for (int64_t t = t1 - 1; t >= t0; --t) {
-            A ca, w;
-            gate_of<GATE>(R::up(a[t * lda + c]), ca, w);
-            lam = fma_of(next, lam, dh ? R::up(dh[t * lddh + c]) : A(0));
-            const bool first = t == t0;
-            const A before = !first ? R::up(h[(t - 1) * ldh + c]) : h0 ? h0[s * n_chan + c] : A(0);
-            if (db)
-                db[t * lddb + c] = R::down(w * lam);
-            if (dz) {
-                A d;
-                if constexpr (GATE == SLA_GATE_VALUE)
-                    d = lam * before;
-                else if constexpr (GATE == SLA_GATE_EXP)
-                    d = lam * before * ca;
-                else {
-                    const A u = R::up(b[t * ldb + c]);
-                    // without a first state the first row is w b alone: its coefficient still weighs b
-                    d = lam * (before - u) * ca * w;
-                }
-                dz[t * lddz + c] = R::down(d);
-            }
-            next = ca;
-        }
-        if (dh0)
-            dh0[s * n_chan + c] = next * lam;
-    }
-}
-
-// Zeros in the rows in front of the first sequence and behind the last one.
-template <typename S>
-__global__ void __launch_bounds__(RT) k_recur_fill(SeqBounds q, int64_t n_chan, S *x, int64_t ldx)
-{
-    const int64_t c = (int64_t)blockIdx.x * RT + threadIdx.x;
-    if (c >= n_chan)
-        return;
-    const int64_t lo = q.at(0), hi = max(lo, q.at(q.n_seq));
-    for (int64_t t = blockIdx.y; t < q.n_tokens; t += gridDim.y)
-        if (t < lo || t >= hi)
-            x[t * ldx + c] = S(0.0f);
-}
 
 template <typename S, int GATE>
 __global__ void __launch_bounds__(RT)
@@ -127,7 +26,7 @@ __global__ void __launch_bounds__(RT)
             continue;
         }
         A ca, w;
-        gate_of<GATE>(R::up(a[r * lda + c]), ca, w);
+        gate_of<GATE, sizeof(S) == 2>(R::up(a[r * lda + c]), ca, w);
         const A v = fma_of(ca, state[i * lds + c], w * R::up(b[r * ldb + c]));
         state[i * lds + c] = v;
         h[r * ldh + c] = R::down(v);
@@ -161,6 +60,14 @@ sla_status check_out(const void *p, int64_t ld, int64_t n_chan)
     return SLA_SUCCESS;
 }
 
+sla_status check_work(int32_t dtype, int64_t n_tokens, int64_t n_chan, const void *d_work, size_t work_bytes)
+{
+    const size_t need = sla_recur_workspace_bytes(dtype, n_tokens, n_chan);
+    if (need && (!d_work || work_bytes < need || (uintptr_t)d_work % 16))
+        return fail(SLA_ERR_INVALID_ARG, "d_work is NULL, smaller than sla_recur_workspace_bytes or not 16-byte aligned");
+    return SLA_SUCCESS;
+}
+
 sla_status check_seqs(int64_t n_tokens, int32_t n_seq, const int32_t *d_seq_off)
 {
     if (n_seq < 0)
@@ -170,22 +77,28 @@ sla_status check_seqs(int64_t n_tokens, int32_t n_seq, const int32_t *d_seq_off)
     return SLA_SUCCESS;
 }
 
-template <class F>
-sla_status with_gate(int32_t gate, F f)
-{
-    switch (gate) {
-    case SLA_GATE_VALUE: return f(std::integral_constant<int, SLA_GATE_VALUE>());
-    case SLA_GATE_EXP: return f(std::integral_constant<int, SLA_GATE_EXP>());
-    default: return f(std::integral_constant<int, SLA_GATE_SIGMOID>());
-    }
-}
-
 dim3 grid_of(int64_t n_chan, int64_t rows)
 {
     return dim3((unsigned)((n_chan + RT - 1) / RT), (unsigned)std::max<int64_t>(1, std::min<int64_t>(rows, 32768)));
 }
 
 }  // namespace
+
+int sm_count()
+{
+    static std::atomic<int> known[64];                     // per device; 0: not asked yet
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return 148;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0)
+        return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+        return 148;
+    if (dev < 64)
+        known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 }  // namespace sla
 
 using namespace sla;
@@ -194,10 +107,11 @@ extern "C" {
 
 size_t sla_recur_workspace_bytes(int32_t dtype, int64_t n_tokens, int64_t n_chan)
 {
-    (void)dtype;
-    (void)n_tokens;
-    (void)n_chan;
-    return 0;
+    if (!row_dtype_ok(dtype) || n_tokens <= 0 || n_chan <= 0 || n_tokens > INT32_MAX || n_chan > INT32_MAX)
+        return 0;
+    // the adjoint's tiles are the shorter ones
+    return dtype == SLA_F64 ? RecurWork<double, SLA_GATE_VALUE, true>::bytes(n_tokens, n_chan)
+                            : RecurWork<float, SLA_GATE_VALUE, true>::bytes(n_tokens, n_chan);
 }
 
 sla_status sla_recur_solve(int32_t dtype, int32_t gate, int64_t n_tokens, int64_t n_chan, int32_t n_seq,
@@ -214,21 +128,23 @@ sla_status sla_recur_solve(int32_t dtype, int32_t gate, int64_t n_tokens, int64_
         SLA_TRY(check_in(d_b, ldb, n_chan));
         SLA_TRY(check_out(d_h, ldh, n_chan));
     }
-    if (work_bytes < sla_recur_workspace_bytes(dtype, n_tokens, n_chan))
-        return fail(SLA_ERR_INVALID_ARG, "d_work is too small");
-    cudaStream_t s = (cudaStream_t)stream;
-    const SeqBounds q{d_seq_off, n_tokens, n_seq};
+    SLA_TRY(check_work(dtype, n_tokens, n_chan, d_work, work_bytes));
     return with_row_type(dtype, [&](auto tag) {
         using S = decltype(tag);
         using A = typename RowType<S>::A;
-        if (flags & SLA_FILL_REST)
-            k_recur_fill<S><<<grid_of(n_chan, n_tokens), RT, 0, s>>>(q, n_chan, (S *)d_h, ldh);
-        return with_gate(gate, [&](auto g) {
-            k_recur_solve<S, decltype(g)::value><<<grid_of(n_chan, n_seq), RT, 0, s>>>(
-                q, n_chan, (const S *)d_a, lda, (const S *)d_b, ldb, (const A *)d_h0, (S *)d_h, ldh, (A *)d_h_last);
-            SLA_CUDA_TRY(cudaGetLastError());
-            return (sla_status)SLA_SUCCESS;
-        });
+        RecurArgs<S> g{};
+        g.q = SeqBounds{d_seq_off, n_tokens, n_seq};
+        g.n_chan = n_chan;
+        g.in[0] = (const S *)d_a;
+        g.in[1] = (const S *)d_b;
+        g.ldin[0] = lda;
+        g.ldin[1] = ldb;
+        g.out[0] = (S *)d_h;
+        g.ldout[0] = ldh;
+        g.enter = (const A *)d_h0;
+        g.leave = (A *)d_h_last;
+        g.fill = (flags & SLA_FILL_REST) != 0;
+        return recur_forward(dtype, gate, &g, d_work, (cudaStream_t)stream);
     });
 }
 
@@ -257,26 +173,34 @@ sla_status sla_recur_adjoint(int32_t dtype, int32_t gate, int64_t n_tokens, int6
         if (d_db)
             SLA_TRY(check_out(d_db, lddb, n_chan));
     }
-    if (work_bytes < sla_recur_workspace_bytes(dtype, n_tokens, n_chan))
-        return fail(SLA_ERR_INVALID_ARG, "d_work is too small");
-    cudaStream_t s = (cudaStream_t)stream;
-    const SeqBounds q{d_seq_off, n_tokens, n_seq};
+    SLA_TRY(check_work(dtype, n_tokens, n_chan, d_work, work_bytes));
     return with_row_type(dtype, [&](auto tag) {
         using S = decltype(tag);
         using A = typename RowType<S>::A;
-        if (flags & SLA_FILL_REST) {
-            if (d_dz)
-                k_recur_fill<S><<<grid_of(n_chan, n_tokens), RT, 0, s>>>(q, n_chan, (S *)d_dz, lddz);
-            if (d_db)
-                k_recur_fill<S><<<grid_of(n_chan, n_tokens), RT, 0, s>>>(q, n_chan, (S *)d_db, lddb);
+        RecurArgs<S> g{};
+        g.q = SeqBounds{d_seq_off, n_tokens, n_seq};
+        g.n_chan = n_chan;
+        g.in[0] = (const S *)d_a;
+        g.ldin[0] = lda;
+        g.in[1] = (const S *)d_dh;
+        g.ldin[1] = lddh;
+        if (d_dz) {
+            g.in[2] = (const S *)d_h;
+            g.ldin[2] = ldh;
+            if (gate == SLA_GATE_SIGMOID) {
+                g.in[3] = (const S *)d_b;
+                g.ldin[3] = ldb;
+            }
         }
-        return with_gate(gate, [&](auto g) {
-            k_recur_adjoint<S, decltype(g)::value><<<grid_of(n_chan, n_seq), RT, 0, s>>>(
-                q, n_chan, (const S *)d_a, lda, (const S *)d_b, ldb, (const S *)d_h, ldh, (const A *)d_h0,
-                (const S *)d_dh, lddh, (const A *)d_dh_last, (S *)d_dz, lddz, (S *)d_db, lddb, (A *)d_dh0);
-            SLA_CUDA_TRY(cudaGetLastError());
-            return (sla_status)SLA_SUCCESS;
-        });
+        g.out[0] = (S *)d_db;
+        g.ldout[0] = lddb;
+        g.out[1] = (S *)d_dz;
+        g.ldout[1] = lddz;
+        g.enter = (const A *)d_dh_last;
+        g.before = (const A *)d_h0;
+        g.leave = (A *)d_dh0;
+        g.fill = (flags & SLA_FILL_REST) != 0;
+        return recur_backward(dtype, gate, &g, d_work, (cudaStream_t)stream);
     });
 }
 

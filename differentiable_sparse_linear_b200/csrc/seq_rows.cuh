@@ -55,25 +55,41 @@ static inline sla_status with_row_type(int32_t dtype, F f)
 static inline bool row_dtype_ok(int32_t dtype) { return dtype >= SLA_F32 && dtype <= SLA_F16; }
 static inline size_t row_bytes(int32_t dtype) { return dtype == SLA_F64 ? 8 : dtype == SLA_F32 ? 4 : 2; }
 
-__device__ __forceinline__ float exp_of(float x) { return expf(x); }
-__device__ __forceinline__ double exp_of(double x) { return exp(x); }
+// sums and products that are never contracted, so that every variant of a loop rounds alike
+__device__ __forceinline__ float add_of(float a, float b) { return __fadd_rn(a, b); }
+__device__ __forceinline__ double add_of(double a, double b) { return __dadd_rn(a, b); }
+__device__ __forceinline__ float mul_of(float a, float b) { return __fmul_rn(a, b); }
+__device__ __forceinline__ double mul_of(double a, double b) { return __dmul_rn(a, b); }
 __device__ __forceinline__ float fma_of(float a, float b, float c) { return __fmaf_rn(a, b, c); }
 __device__ __forceinline__ double fma_of(double a, double b, double c) { return __fma_rn(a, b, c); }
 
+// exp and 1 / (1 + e) of a gate, e in [0, 1].  Rows of 16 bits take the hardware's exp2 and reciprocal
+// (__expf: (2 + 1.2 |x|) 2^-23 relative): z itself was rounded to 2^-9 |z| (bf16) or 2^-12 |z| (fp16), so
+// its coefficient is already uncertain by over 100 times that, and the exact functions' extra
+// instructions would show at one pass over memory.
+template <bool FAST>
+__device__ __forceinline__ float gate_exp(float x) { return FAST ? __expf(x) : expf(x); }
+template <bool FAST>
+__device__ __forceinline__ double gate_exp(double x) { return exp(x); }
+template <bool FAST>
+__device__ __forceinline__ float gate_rcp(float x) { return FAST ? __fdividef(1.0f, x) : __frcp_rn(x); }
+template <bool FAST>
+__device__ __forceinline__ double gate_rcp(double x) { return 1.0 / x; }
+
 // Coefficient a and input weight w of a stored gate value z.  The sigmoid's two halves come from
 // one e = exp(-|z|): 1/(1+e) and e/(1+e), so that 1 - a keeps its digits where a rounds to 1.
-template <int GATE, typename A>
+template <int GATE, bool FAST, typename A>
 __device__ __forceinline__ void gate_of(A z, A &a, A &w)
 {
     if constexpr (GATE == SLA_GATE_VALUE) {
         a = z;
         w = A(1);
     } else if constexpr (GATE == SLA_GATE_EXP) {
-        a = exp_of(z);
+        a = gate_exp<FAST>(z);
         w = A(1);
     } else {
-        const A e = exp_of(z < A(0) ? z : -z);
-        const A big = A(1) / (A(1) + e), small = e * big;
+        const A e = gate_exp<FAST>(z < A(0) ? z : -z);
+        const A big = gate_rcp<FAST>(A(1) + e), small = e * big;
         a = z < A(0) ? small : big;
         w = z < A(0) ? big : small;
     }
