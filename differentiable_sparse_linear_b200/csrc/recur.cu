@@ -109,9 +109,9 @@ size_t sla_recur_workspace_bytes(int32_t dtype, int64_t n_tokens, int64_t n_chan
 {
     if (!row_dtype_ok(dtype) || n_tokens <= 0 || n_chan <= 0 || n_tokens > INT32_MAX || n_chan > INT32_MAX)
         return 0;
-    // the adjoint's tiles are the shorter ones
-    return dtype == SLA_F64 ? RecurWork<double, SLA_GATE_VALUE, true>::bytes(n_tokens, n_chan)
-                            : RecurWork<float, SLA_GATE_VALUE, true>::bytes(n_tokens, n_chan);
+    // the tiles of the adjoint with the sigmoid gate are the shortest ones
+    return dtype == SLA_F64 ? RecurWork<double, SLA_GATE_SIGMOID, true>::bytes(n_tokens, n_chan)
+                            : RecurWork<float, SLA_GATE_SIGMOID, true>::bytes(n_tokens, n_chan);
 }
 
 sla_status sla_recur_solve(int32_t dtype, int32_t gate, int64_t n_tokens, int64_t n_chan, int32_t n_seq,

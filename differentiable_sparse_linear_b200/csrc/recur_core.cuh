@@ -7,16 +7,17 @@
 // result from a zero state), and runs compose by (A2 A1, A2 H1 + H2).
 //
 // Layout.  A tile is C scan positions (rows in scan order; backward counts from the last row)
-// times 128 bytes of channels.  A compute thread owns R = 4 consecutive positions of 16 bytes of channels; the
-// 4 threads of a warp that share channels own 16 consecutive positions, the NW warps the tile.
-// Tiles are taken by ticket, chunk-major, by one persistent block per SM.
+// times 128 bytes of channels.  A compute thread owns a run of R = 4 consecutive positions of 16 bytes of channels;
+// 8 threads make a row, so the tile has NR = 4 NW runs.  Tiles are taken by ticket, chunk-major, by
+// one persistent block per SM.
 //
 // One block runs four kinds of work at the same time, tile i being the oldest:
 //   loads       each thread copies its own rows of tile i + NS into its own place in shared memory
 //               (cp.async), so staging needs no barrier;
-//   pass 1      tile i + 1: each thread's (A, H), combined over the warp, given to the scan warps;
-//   scan warps  tile i + 1, one thread a channel: the tile's (A, H), published for later chunks; the state
-//               that enters it, from the published results of earlier chunks; the state that enters every warp;
+//   pass 1      tile i + 1: each thread's (A, H), left in shared memory;
+//   scan warps  tile i + 1, one thread a channel, over the runs in order: the tile's (A, H), published for
+//               later chunks; the state that enters it, from the published results of earlier
+//               chunks; the state that enters every run;
 //   pass 2      tile i: every row from the state that enters it, in the order of the formula, and the stores.
 // A plan warp takes the tickets and finds the sequence borders inside a tile, NS tiles ahead.  So each
 // input is read once and the wait on earlier chunks passes while other tiles are worked on.
@@ -86,11 +87,12 @@ struct RecurShape {
     static constexpr int V = 16 / (int)sizeof(S);          // channels of a thread
     static constexpr int W = 8 * V;                        // channels of a tile
     static constexpr int R = 4;
-    // Warps and stages that fill shared memory: two inputs 12 warps x 4 stages (C = 192), three 8 x 4, four 8 x 3 (C = 128).
-    static constexpr int NW = REV ? 8 : 12;
-    static constexpr int NS = NIN == 4 ? 3 : 4;
+    // Warps and stages by shared memory (three stages, so that a load has a tile's time to arrive)
+    static constexpr int NW = !REV ? 12 : NIN == 3 ? 10 : 7;
+    static constexpr int NS = 3;
     static constexpr int NP = NS + 1;                      // plan slots
-    static constexpr int C = NW * 16;
+    static constexpr int NR = NW * 4;                      // runs
+    static constexpr int C = NR * R;
     static constexpr int NC = NW * 32;                     // compute threads
     static constexpr int NSCAN = (W + 31) / 32 * 32;
     static constexpr int NT = NC + NSCAN + 32;
@@ -108,8 +110,8 @@ struct RecurSmem {
     using P = RecurShape<S, GATE, REV>;
     using A = typename RowType<S>::A;
     uint4 stage[P::NS][P::NIN][P::R][P::NC];
-    A aggA[2][P::NW][P::W], aggH[2][P::NW][P::W];
-    A hs[2][P::NW][P::W];
+    // per run and channel (A, H); the scan leaves the state that enters the run in H's place
+    A mapA[2][P::NR][P::W], mapH[2][P::NR][P::W];
     int begin[P::NP][P::C], finish[P::NP][P::C];   // sequence the scan enters / leaves at a position, or -1
     TilePlan plan[P::NP];
 };
@@ -303,16 +305,42 @@ struct Recur {
     const RecurArgs<S> &g;
     Sm &sm;
     const int tid, warp, lane, l8;
-    const int p0;                                          // first position of the thread in a tile
+    const int run;                                         // the thread's run of a tile
+    const int p0;                                          // its first position
 
     __device__ __forceinline__ Recur(const RecurArgs<S> &g_, Sm &sm_)
         : g(g_), sm(sm_), tid(threadIdx.x), warp(tid >> 5), lane(tid & 31), l8(lane & 7),
-          p0(warp * 16 + (lane >> 3) * R)
+          run(tid >> 3), p0(run * R)
     {
     }
 
     // local channel of element v of the thread
     __device__ __forceinline__ int chan(int v) const { return ((v / U) * 8 + l8) * U + v % U; }
+    // place of a thread's 16 bytes of channels, and of one channel, in a row of the maps: element v of
+    // lane l8 is at (v / Q) 8 Q + l8 Q + v % Q, so that 16-byte accesses of 8 lanes are contiguous
+    static constexpr int Q = 16 / (int)sizeof(A);
+    static __device__ __forceinline__ int chan_at(int place)
+    {
+        const int v = place / (8 * Q) * Q + place % Q, l = place / Q % 8;
+        return ((v / U) * 8 + l) * U + v % U;
+    }
+    __device__ __forceinline__ void put_map(A (*m)[P::W], const A (&x)[V]) const
+    {
+#pragma unroll
+        for (int j = 0; j < V / Q; ++j) {
+            uint4 w;
+            memcpy(&w, &x[j * Q], 16);
+            *reinterpret_cast<uint4 *>(&m[run][j * 8 * Q + l8 * Q]) = w;
+        }
+    }
+    __device__ __forceinline__ void get_map(A (*m)[P::W], A (&x)[V]) const
+    {
+#pragma unroll
+        for (int j = 0; j < V / Q; ++j) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(&m[run][j * 8 * Q + l8 * Q]);
+            memcpy(&x[j * Q], &w, 16);
+        }
+    }
     __device__ __forceinline__ int64_t row_of(const TilePlan &pl, int p) const
     {
         const int64_t pos = (int64_t)pl.chunk * C + p;
@@ -322,70 +350,71 @@ struct Recur {
     __device__ __forceinline__ bool reads(int k) const { return g.in[k] != nullptr; }
 
     // start the copies of the thread's rows of a tile
+    template <bool SEG>
+    __device__ __forceinline__ void load_rows(const TilePlan &pl, int st)
+    {
+        const int64_t c0 = (int64_t)pl.cb * P::W;
+        const int64_t t0 = row_of(pl, p0);
+#pragma unroll
+        for (int k = 0; k < P::NIN; ++k) {
+            if (!reads(k))
+                continue;
+            const int back = REV && k == 2;                // the state before the row
+            const S *src = g.in[k] + (t0 - back) * g.ldin[k] + c0;
+            const int64_t step = REV ? -g.ldin[k] : g.ldin[k];
+#pragma unroll
+            for (int i = 0; i < R; ++i, src += step) {
+                const int p = p0 + i;
+                if (SEG && (p < pl.lo || p >= pl.hi))
+                    continue;
+                if (back && t0 - i <= 0)
+                    continue;
+                S *dst = reinterpret_cast<S *>(&sm.stage[st][k][i][tid]);
+#pragma unroll
+                for (int j = 0; j < UNITS; ++j) {
+                    const int c = chan(j * U);
+                    const int64_t left = g.n_chan - c0 - c;
+                    if (left <= 0)
+                        continue;
+                    if constexpr (U * sizeof(S) >= 4)
+                        copy_async<U * (int)sizeof(S)>(dst + j * U, src + c, (int)min(left, (int64_t)U) * (int)sizeof(S));
+                    else
+                        dst[j] = src[c];
+                }
+            }
+        }
+    }
     __device__ __forceinline__ void load(const TilePlan &pl, int st)
     {
         if (pl.tile >= 0) {
-            const int64_t c0 = (int64_t)pl.cb * P::W;
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const int p = p0 + i;
-                if (p < pl.lo || p >= pl.hi)
-                    continue;
-                const int64_t t = row_of(pl, p);
-#pragma unroll
-                for (int k = 0; k < P::NIN; ++k) {
-                    if (!reads(k))
-                        continue;
-                    const int64_t row = REV && k == 2 ? t - 1 : t;   // the state before the row
-                    if (row < 0)
-                        continue;
-                    const S *src = g.in[k] + row * g.ldin[k] + c0;
-                    S *dst = reinterpret_cast<S *>(&sm.stage[st][k][i][tid]);
-#pragma unroll
-                    for (int j = 0; j < UNITS; ++j) {
-                        const int c = chan(j * U);
-                        const int64_t left = g.n_chan - c0 - c;
-                        if (left <= 0)
-                            continue;
-                        if constexpr (U * sizeof(S) >= 4)
-                            copy_async<U * (int)sizeof(S)>(dst + j * U, src + c, (int)min(left, (int64_t)U) * (int)sizeof(S));
-                        else
-                            dst[j] = src[c];
-                    }
-                }
-            }
+            if (pl.seg)
+                load_rows<true>(pl, st);
+            else
+                load_rows<false>(pl, st);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
 
-    struct Row {
-        uint4 raw;
-        __device__ __forceinline__ A operator[](int v) const
-        {
-            S s[V];
-            memcpy(s, &raw, 16);
-            return RT::up(s[v]);
-        }
-    };
-    __device__ __forceinline__ Row staged(int st, int k, int i) const
+    __device__ __forceinline__ void staged(int st, int k, int i, A (&x)[V]) const
     {
-        Row r;
-        r.raw = reads(k) ? sm.stage[st][k][i][tid] : make_uint4(0, 0, 0, 0);
-        return r;
+        const uint4 r = reads(k) ? sm.stage[st][k][i][tid] : make_uint4(0, 0, 0, 0);
+        unpack16(r, x, S());
     }
     __device__ __forceinline__ A enter_of(int s, int64_t ch) const
     {
         return g.enter && ch < g.n_chan ? g.enter[(int64_t)s * g.n_chan + ch] : A(0);
     }
 
-    // (A, H) of the thread's rows; left in (ea, eh) as the map of the warp's rows in front of them
+    // (A, H) of the thread's rows
     template <bool SEG>
     __device__ __forceinline__ void pass1_rows(const TilePlan &pl, int slot, int st, A (&ma)[V], A (&mh)[V])
     {
         const int64_t c0 = (int64_t)pl.cb * P::W;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const Row z = staged(st, 0, i), x = staged(st, 1, i);
+            A z[V], x[V];
+            staged(st, 0, i, z);
+            staged(st, 1, i, x);
             const int p = p0 + i;
             int s = -1;
             bool inside = true;
@@ -425,56 +454,36 @@ struct Recur {
         }
     }
 
-    __device__ __forceinline__ void pass1(const TilePlan &pl, int slot, int st, int buf, A (&ea)[V], A (&eh)[V])
+    __device__ __forceinline__ void pass1(const TilePlan &pl, int slot, int st, int buf)
     {
         A ma[V], mh[V];
         if (pl.seg)
             pass1_rows<true>(pl, slot, st, ma, mh);
         else
             pass1_rows<false>(pl, slot, st, ma, mh);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            // inclusive over the warp's four runs of these channels
-#pragma unroll
-            for (int d = 8; d < 32; d *= 2) {
-                const A oa = __shfl_up_sync(0xffffffffu, ma[v], d), oh = __shfl_up_sync(0xffffffffu, mh[v], d);
-                if (lane >= d) {
-                    mh[v] = apply(ma[v], oh, mh[v]);
-                    ma[v] = product(ma[v], oa);
-                }
-            }
-            const A xa = __shfl_up_sync(0xffffffffu, ma[v], 8), xh = __shfl_up_sync(0xffffffffu, mh[v], 8);
-            ea[v] = lane < 8 ? A(1) : xa;
-            eh[v] = lane < 8 ? A(0) : xh;
-            if (lane >= 24) {
-                sm.aggA[buf][warp][chan(v)] = ma[v];
-                sm.aggH[buf][warp][chan(v)] = mh[v];
-            }
-        }
+        put_map(sm.mapA[buf], ma);
+        put_map(sm.mapH[buf], mh);
     }
 
     __device__ __forceinline__ void store(int k, int64_t t, int64_t c0, const A (&x)[V])
     {
-        S s[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            s[v] = RT::down(x[v]);
         S *dst = g.out[k] + t * g.ldout[k] + c0;
+        const uint4 r = pack16(x, S());
+        S s[V];
+        memcpy(s, &r, 16);
 #pragma unroll
         for (int j = 0; j < UNITS; ++j) {
             const int c = chan(j * U);
             const int64_t left = g.n_chan - c0 - c;
             if (left >= U) {
-                if constexpr (U == 1)
+                if constexpr (UNITS == 1)
+                    *reinterpret_cast<uint4 *>(dst + c) = r;
+                else if constexpr (U == 1)
                     dst[c] = s[j];
-                else if constexpr (U * sizeof(S) == 4) {
+                else {
                     unsigned w;
                     memcpy(&w, s + j * U, 4);
                     *reinterpret_cast<unsigned *>(dst + c) = w;
-                } else {
-                    uint4 w;
-                    memcpy(&w, s, 16);
-                    *reinterpret_cast<uint4 *>(dst + c) = w;
                 }
             } else if constexpr (U > 1) {
 #pragma unroll
@@ -510,7 +519,9 @@ struct Recur {
                 s = sm.begin[slot][p];
                 f = sm.finish[slot][p];
             }
-            const Row z = staged(st, 0, i), y = staged(st, 1, i);
+            A z[V], y[V];
+            staged(st, 0, i, z);
+            staged(st, 1, i, y);
             if constexpr (!REV) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
@@ -524,8 +535,10 @@ struct Recur {
                 }
                 store(0, t, c0, x);
             } else {
-                const Row hb = staged(st, 2, i);
-                A db[V], dz[V];
+                A hb[V], u[V], db[V], dz[V];
+                staged(st, 2, i, hb);
+                if constexpr (GATE == SLA_GATE_SIGMOID)
+                    staged(st, 3, i, u);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     A a, w;
@@ -543,7 +556,7 @@ struct Recur {
                     else if constexpr (GATE == SLA_GATE_EXP)
                         dz[v] = x[v] * hp;
                     else
-                        dz[v] = x[v] * w * (hp - staged(st, 3, i)[v]);
+                        dz[v] = x[v] * w * (hp - u[v]);
                 }
                 if (g.out[0])
                     store(0, t, c0, db);
@@ -561,38 +574,86 @@ struct Recur {
         }
     }
 
-    __device__ __forceinline__ void pass2(const TilePlan &pl, int slot, int st, int buf, const A (&ea)[V], const A (&eh)[V])
+    __device__ __forceinline__ void pass2(const TilePlan &pl, int slot, int st, int buf)
     {
         A x[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            x[v] = apply(ea[v], sm.hs[buf][warp][chan(v)], eh[v]);
+        get_map(sm.mapH[buf], x);
         if (pl.seg)
             pass2_rows<true>(pl, slot, st, x);
         else
             pass2_rows<false>(pl, slot, st, x);
     }
 
-    // one channel of a tile: publish, find the state that enters, hand it to the warps
-    __device__ __forceinline__ void scan(const TilePlan &pl, int slot, int buf, int c)
+    // The tile's (A, H) of one channel.  Without borders in the tile no map is constant, and the guard
+    // against an overflowed A times 0 is needed only if a NaN came out.  The products of four runs fit
+    // fp32 (16 coefficients), the tile's is taken in fp64.
+    template <bool GUARD>
+    __device__ __forceinline__ void tile_map(int buf, int place, double &ta, A &th) const
+    {
+        ta = 1.0;
+        th = A(0);
+        for (int q = 0; q < P::NR; q += 8) {
+            A a[8], h[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (q + k < P::NR) {
+                    a[k] = sm.mapA[buf][q + k][place];
+                    h[k] = sm.mapH[buf][q + k][place];
+                }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (q + k < P::NR)
+                    th = GUARD ? apply(a[k], th, h[k]) : fma_of(a[k], th, h[k]);
+#pragma unroll
+            for (int k = 0; k < 8; k += 4)
+                if (q + k < P::NR) {
+                    if constexpr (GUARD)
+                        ta = product((double)product(product(a[k + 3], a[k + 2]), product(a[k + 1], a[k])), ta);
+                    else
+                        ta *= (double)((a[k + 3] * a[k + 2]) * (a[k + 1] * a[k]));
+                }
+        }
+        ta = is_const(ta) && GUARD ? ta : ta + 0.0;
+    }
+    // Every run gets the state that enters it.
+    template <bool GUARD>
+    __device__ __forceinline__ A enter_runs(int buf, int place, A x)
+    {
+        for (int q = 0; q < P::NR; q += 8) {
+            A a[8], h[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (q + k < P::NR) {
+                    a[k] = sm.mapA[buf][q + k][place];
+                    h[k] = sm.mapH[buf][q + k][place];
+                }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (q + k < P::NR) {
+                    sm.mapH[buf][q + k][place] = x;
+                    x = GUARD ? apply(a[k], x, h[k]) : fma_of(a[k], x, h[k]);
+                }
+        }
+        return x;
+    }
+
+    // one channel of a tile: publish, find the state that enters, hand it to the runs
+    __device__ __forceinline__ void scan(const TilePlan &pl, int slot, int buf, int place)
     {
         using Wd = Words<A>;
-        const int64_t ch = (int64_t)pl.cb * P::W + c;
-        A a[P::NW], h[P::NW];
-#pragma unroll
-        for (int w = 0; w < P::NW; ++w) {
-            a[w] = sm.aggA[buf][w][c];
-            h[w] = sm.aggH[buf][w][c];
+        const int64_t ch = (int64_t)pl.cb * P::W + chan_at(place);
+        if (ch >= g.n_chan)
+            return;
+        double ta;
+        A th, x = A(0);
+        if (pl.seg)
+            tile_map<true>(buf, place, ta, th);
+        else {
+            tile_map<false>(buf, place, ta, th);
+            if (!(th == th))
+                tile_map<true>(buf, place, ta, th);
         }
-        A x = A(0);
-        if (g.n_chunks > 1 && ch < g.n_chan) {
-            double ta = a[0];
-            A th = h[0];
-#pragma unroll
-            for (int w = 1; w < P::NW; ++w) {
-                th = apply(a[w], th, h[w]);
-                ta = product((double)a[w], ta);
-            }
+        if (g.n_chunks > 1) {
             ta = Wd::round_a(ta);
             const int64_t at = (int64_t)pl.chunk * g.n_chan + ch;
             typename Wd::Inc *inc = (typename Wd::Inc *)g.inc;
@@ -610,11 +671,12 @@ struct Recur {
                     st_word(inc + at, Wd::inc_bits(apply_wide(ta, x, th)));
             }
         }
-#pragma unroll
-        for (int w = 0; w < P::NW; ++w) {
-            sm.hs[buf][w][c] = x;
-            x = apply(a[w], x, h[w]);
-        }
+        // The guard is needed with constant maps, and where a run's A overflowed, which leaves the tile's
+        // not finite.
+        if (pl.seg || !isfinite(ta))
+            enter_runs<true>(buf, place, x);
+        else
+            enter_runs<false>(buf, place, x);
     }
 
     // the plan warp: the next tile, and where sequences begin and end in it
@@ -699,7 +761,7 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
 {
     using P = RecurShape<S, GATE, REV>;
     using A = typename RowType<S>::A;
-    constexpr int V = P::V, NS = P::NS, NP = P::NP;
+    constexpr int NS = P::NS, NP = P::NP;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     RecurSmem<S, GATE, REV> &sm = *reinterpret_cast<RecurSmem<S, GATE, REV> *>(smem_raw);
     Recur<S, GATE, U, REV> r(g, sm);
@@ -710,10 +772,9 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
             r.load(sm.plan[j], j);
             __syncwarp();
         }
-        A ea[V], eh[V], na[V], nh[V];
         asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
         if (sm.plan[0].tile >= 0)
-            r.pass1(sm.plan[0], 0, 0, 0, ea, eh);
+            r.pass1(sm.plan[0], 0, 0, 0);
         __syncwarp();
         bar_arrive(BAR_P1, P::NC + P::NSCAN);
         int st = 0, slot = 0, buf = 0;
@@ -721,20 +782,15 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
             const int st1 = st + 1 == NS ? 0 : st + 1, slot1 = slot + 1 == NP ? 0 : slot + 1;
             asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
             if (sm.plan[slot1].tile >= 0)
-                r.pass1(sm.plan[slot1], slot1, st1, buf ^ 1, na, nh);
+                r.pass1(sm.plan[slot1], slot1, st1, buf ^ 1);
             __syncwarp();
             bar_arrive(BAR_P1 + (buf ^ 1), P::NC + P::NSCAN);
             bar_sync(BAR_P2 + buf, P::NC + P::NSCAN);
-            r.pass2(sm.plan[slot], slot, st, buf, ea, eh);
+            r.pass2(sm.plan[slot], slot, st, buf);
             __syncwarp();
             bar_sync(BAR_PLAN, P::NC + 32);
             const int ahead = slot + NS >= NP ? slot + NS - NP : slot + NS;
             r.load(sm.plan[ahead], st);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                ea[v] = na[v];
-                eh[v] = nh[v];
-            }
             st = st1;
             slot = slot1;
             buf ^= 1;

@@ -63,21 +63,95 @@ __device__ __forceinline__ double mul_of(double a, double b) { return __dmul_rn(
 __device__ __forceinline__ float fma_of(float a, float b, float c) { return __fmaf_rn(a, b, c); }
 __device__ __forceinline__ double fma_of(double a, double b, double c) { return __fma_rn(a, b, c); }
 
-// exp and 1 / (1 + e) of a gate, e in [0, 1].  Rows of 16 bits take the hardware's exp2 and reciprocal
-// (__expf: (2 + 1.2 |x|) 2^-23 relative): z itself was rounded to 2^-9 |z| (bf16) or 2^-12 |z| (fp16), so
-// its coefficient is already uncertain by over 100 times that, and the exact functions' extra
-// instructions would show at one pass over memory.
+// 16 bytes of a row <-> arithmetic values.
+__device__ __forceinline__ void unpack16(const uint4 &r, float (&x)[4], float)
+{
+    x[0] = __uint_as_float(r.x);
+    x[1] = __uint_as_float(r.y);
+    x[2] = __uint_as_float(r.z);
+    x[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ void unpack16(const uint4 &r, double (&x)[2], double)
+{
+    x[0] = __hiloint2double((int)r.y, (int)r.x);
+    x[1] = __hiloint2double((int)r.w, (int)r.z);
+}
+__device__ __forceinline__ void unpack16(const uint4 &r, float (&x)[8], __nv_bfloat16)
+{
+    const unsigned w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack16(const uint4 &r, float (&x)[8], __half)
+{
+    const unsigned w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ uint4 pack16(const float (&x)[4], float)
+{
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+__device__ __forceinline__ uint4 pack16(const double (&x)[2], double)
+{
+    return make_uint4((unsigned)__double2loint(x[0]), (unsigned)__double2hiint(x[0]), (unsigned)__double2loint(x[1]),
+                      (unsigned)__double2hiint(x[1]));
+}
+__device__ __forceinline__ uint4 pack16(const float (&x)[8], __nv_bfloat16)
+{
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const unsigned *>(&p);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack16(const float (&x)[8], __half)
+{
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 p = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const unsigned *>(&p);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// exp and 1 / (1 + e) of a gate.  Rows of 16 bits take the hardware's exp2 directly (2^-22 relative and
+// 2^-24 |x log2 e| from rounding its argument): z itself was rounded by 2^-9 |z| (bf16) or 2^-12 |z| (fp16),
+// so its coefficient is already uncertain by over 100 times that, and the exact function's extra
+// instructions would show at one pass over memory.  The hardware's reciprocal is 2^-23 relative.
 template <bool FAST>
-__device__ __forceinline__ float gate_exp(float x) { return FAST ? __expf(x) : expf(x); }
+__device__ __forceinline__ float gate_exp(float x)
+{
+    if constexpr (FAST) {
+        float r;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+        return r;
+    } else
+        return expf(x);
+}
 template <bool FAST>
 __device__ __forceinline__ double gate_exp(double x) { return exp(x); }
-template <bool FAST>
-__device__ __forceinline__ float gate_rcp(float x) { return FAST ? __fdividef(1.0f, x) : __frcp_rn(x); }
-template <bool FAST>
+__device__ __forceinline__ float gate_rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ double gate_rcp(double x) { return 1.0 / x; }
 
-// Coefficient a and input weight w of a stored gate value z.  The sigmoid's two halves come from
-// one e = exp(-|z|): 1/(1+e) and e/(1+e), so that 1 - a keeps its digits where a rounds to 1.
+// Coefficient a and input weight w of a stored gate value z.  Both halves of the sigmoid come from
+// one e = exp(-z), a = 1 / (1 + e) and w = e a, so that 1 - a keeps its digits where a rounds to 1.  z
+// is held above -86 (fp64: -700), where e would leave the range and a is below 1e-37 anyway.
 template <int GATE, bool FAST, typename A>
 __device__ __forceinline__ void gate_of(A z, A &a, A &w)
 {
@@ -88,10 +162,10 @@ __device__ __forceinline__ void gate_of(A z, A &a, A &w)
         a = gate_exp<FAST>(z);
         w = A(1);
     } else {
-        const A e = gate_exp<FAST>(z < A(0) ? z : -z);
-        const A big = gate_rcp<FAST>(A(1) + e), small = e * big;
-        a = z < A(0) ? small : big;
-        w = z < A(0) ? big : small;
+        const A floor = sizeof(A) == 4 ? A(-86) : A(-700);
+        const A e = gate_exp<FAST>(-(z < floor ? floor : z));   // a NaN stays one
+        a = gate_rcp(A(1) + e);
+        w = e * a;
     }
 }
 
