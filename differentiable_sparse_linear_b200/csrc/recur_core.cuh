@@ -15,9 +15,9 @@
 //   loads       each thread copies its own rows of tile i + NS into its own place in shared memory
 //               (cp.async), so staging needs no barrier;
 //   pass 1      tile i + 1: each thread's (A, H), left in shared memory;
-//   scan warps  tile i + 1, one thread a channel, over the runs in order: the tile's (A, H), published for
-//               later chunks; the state that enters it, from the published results of earlier
-//               chunks; the state that enters every run;
+//   scan warps  tile i + 1, four threads a channel, each over a quarter of the runs in order: the tile's (A, H),
+//               published for later chunks; the state that enters it, from the published results of
+//               earlier chunks; the state that enters every run;
 //   pass 2      tile i: every row from the state that enters it, in the order of the formula, and the stores.
 // A plan warp takes the tickets and finds the sequence borders inside a tile, NS tiles ahead.  So each
 // input is read once and the wait on earlier chunks passes while other tiles are worked on.
@@ -94,7 +94,8 @@ struct RecurShape {
     static constexpr int NR = NW * 4;                      // runs
     static constexpr int C = NR * R;
     static constexpr int NC = NW * 32;                     // compute threads
-    static constexpr int NSCAN = (W + 31) / 32 * 32;
+    static constexpr int RQ = NR / 4;                      // runs of a quarter of the tile
+    static constexpr int NSCAN = W * 4;                    // scan threads: four a channel, a quarter each
     static constexpr int NT = NC + NSCAN + 32;
 };
 
@@ -235,61 +236,97 @@ struct Words<double> {
     static __device__ __forceinline__ bool inc_there(unsigned long long v) { return v != NONE; }
 };
 
-// The state that enters `chunk` at one channel: back to the nearest chunk whose leaving state is there
-// (WIN chunks a round trip), then forward over the maps behind it.
+// The state that enters `chunk` at one channel, by the four lanes l, l + 8, l + 16, l + 24 of a warp: back to the
+// nearest chunk whose leaving state is there (4 K chunks a round trip, K a lane), then forward over the
+// maps behind it, one after the other.  All lanes of the warp call it; `want` is false where no state is needed.
 template <typename A>
-__device__ __forceinline__ A state_before(int chunk, int64_t n_chan, int64_t ch, const unsigned long long *agg,
-                                          const typename Words<A>::Inc *inc)
+__device__ __forceinline__ A state_before(int chunk, int64_t n_chan, int64_t ch, bool want, int lane,
+                                          const unsigned long long *agg, const typename Words<A>::Inc *inc)
 {
     using Wd = Words<A>;
-    constexpr int WIN = 12 / Wd::N;
+    constexpr int K = 4, OPEN = 1 << 20;
+    const unsigned all = 0xffffffffu;
+    const int q = lane >> 3, l8 = lane & 7;
+    bool done = !want, gave_up = false;
     A x = A(0);
-    int last = chunk - 1, from = -1;
-    for (int polls = 0; polls < (1 << 22); ++polls) {
-        typename Wd::Inc v[WIN];
-        Wd m[WIN];
+    int last = chunk - 1, from = chunk;
+    for (int polls = 0;; ++polls) {
+        typename Wd::Inc v[K];
+        Wd m[K];
+        int mine = OPEN;               // 2 * (distance) of the nearest leaving state, + 1 if a map is missing first
+        if (!done) {
 #pragma unroll
-        for (int k = 0; k < WIN; ++k) {
-            const int64_t at = (int64_t)max(last - k, 0) * n_chan + ch;
-            v[k] = ld_word(inc + at);
-            m[k].load(agg + at * Wd::N);
+            for (int k = 0; k < K; ++k) {
+                const int64_t at = (int64_t)max(last - q * K - k, 0) * n_chan + ch;
+                v[k] = ld_word(inc + at);
+                m[k].load(agg + at * Wd::N);
+            }
+#pragma unroll
+            for (int k = K - 1; k >= 0; --k)
+                if (last - q * K - k >= 0) {
+                    if (Wd::inc_there(v[k]))
+                        mine = 2 * (q * K + k);
+                    else if (!m[k].there())
+                        mine = 2 * (q * K + k) + 1;
+                }
         }
-        int found = -1;
-        bool open = true;              // every map nearer than k is there
+        mine = min(mine, __shfl_xor_sync(all, mine, 8));
+        mine = min(mine, __shfl_xor_sync(all, mine, 16));
+        const bool found = !done && mine < OPEN && !(mine & 1);
+        if (__any_sync(all, found)) {
+            const int fq = mine / 2 / K, fk = mine / 2 % K;
+            A y = A(0);
 #pragma unroll
-        for (int k = 0; k < WIN; ++k) {
-            if (open && found < 0 && last - k >= 0) {
-                if (Wd::inc_there(v[k])) {
-                    found = k;
-                    x = Wd::inc_value(v[k]);
-                } else
-                    open = m[k].there();
+            for (int k = 0; k < K; ++k)
+                if (found && q == fq && k == fk)
+                    y = Wd::inc_value(v[k]);
+#pragma unroll
+            for (int s = 3; s >= 0; --s) {
+                if (found && q == s && s <= fq) {
+#pragma unroll
+                    for (int k = K - 1; k >= 0; --k)
+                        if (s < fq || k < fk)
+                            y = apply_wide(m[k].a(), y, m[k].h());
+                }
+                const A o = __shfl_sync(all, y, s * 8 + l8);
+                if (q < s && s <= fq)
+                    y = o;
+            }
+            y = __shfl_sync(all, y, l8);
+            if (found) {
+                x = y;
+                from = last + 1;
+                done = true;
             }
         }
-        if (found >= 0) {
-#pragma unroll
-            for (int k = WIN - 1; k >= 0; --k)
-                if (k < found)
-                    x = apply_wide(m[k].a(), x, m[k].h());
-            from = last + 1;
+        if (!done && mine == OPEN && last - 4 * K >= 0)
+            last -= 4 * K;
+        if (!__any_sync(all, !done))
+            break;
+        if (polls >= 1 << 22) {
+            gave_up = !done;
             break;
         }
-        if (open && last - WIN >= 0)
-            last -= WIN;
     }
-    if (from < 0)
-        return A(NAN);                 // gave up
-    for (; from < chunk; from += WIN) {
-        Wd m[WIN];
+    // the maps that were passed on the way back
+    while (__any_sync(all, from < chunk)) {
+        Wd m[K];
 #pragma unroll
-        for (int k = 0; k < WIN; ++k)
-            m[k].load(agg + ((int64_t)min(from + k, chunk - 1) * n_chan + ch) * Wd::N);
+        for (int k = 0; k < K; ++k)
+            m[k].load(agg + ((int64_t)min(from + q * K + k, chunk - 1) * n_chan + ch) * Wd::N);
 #pragma unroll
-        for (int k = 0; k < WIN; ++k)
-            if (from + k < chunk)
-                x = apply_wide(m[k].a(), x, m[k].h());
+        for (int s = 0; s < 4; ++s) {
+            if (q == s) {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (from + q * K + k < chunk)
+                        x = apply_wide(m[k].a(), x, m[k].h());
+            }
+            x = __shfl_sync(all, x, s * 8 + l8);
+        }
+        from += 4 * K;
     }
-    return x;
+    return gave_up ? A(NAN) : x;
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -316,9 +353,11 @@ struct Recur {
 
     // local channel of element v of the thread
     __device__ __forceinline__ int chan(int v) const { return ((v / U) * 8 + l8) * U + v % U; }
-    // place of a thread's 16 bytes of channels, and of one channel, in a row of the maps: element v of
-    // lane l8 is at (v / Q) 8 Q + l8 Q + v % Q, so that 16-byte accesses of 8 lanes are contiguous
+    // Place of a thread's 16 bytes of channels, and of one channel, in a row of the maps: element v of
+    // lane l8 is at (v / Q) 8 Q + l8 Q + v % Q, so that 16-byte accesses of 8 lanes are contiguous; a quarter's
+    // rows are turned by 8 places, so that a scan warp (8 places of four quarters) meets no bank twice.
     static constexpr int Q = 16 / (int)sizeof(A);
+    static __device__ __forceinline__ int turn(int quarter) { return (quarter * 8) & (P::W - 1); }
     static __device__ __forceinline__ int chan_at(int place)
     {
         const int v = place / (8 * Q) * Q + place % Q, l = place / Q % 8;
@@ -330,14 +369,14 @@ struct Recur {
         for (int j = 0; j < V / Q; ++j) {
             uint4 w;
             memcpy(&w, &x[j * Q], 16);
-            *reinterpret_cast<uint4 *>(&m[run][j * 8 * Q + l8 * Q]) = w;
+            *reinterpret_cast<uint4 *>(&m[run][(j * 8 * Q + l8 * Q) ^ turn(run / P::RQ)]) = w;
         }
     }
     __device__ __forceinline__ void get_map(A (*m)[P::W], A (&x)[V]) const
     {
 #pragma unroll
         for (int j = 0; j < V / Q; ++j) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(&m[run][j * 8 * Q + l8 * Q]);
+            const uint4 w = *reinterpret_cast<const uint4 *>(&m[run][(j * 8 * Q + l8 * Q) ^ turn(run / P::RQ)]);
             memcpy(&x[j * Q], &w, 16);
         }
     }
@@ -584,99 +623,105 @@ struct Recur {
             pass2_rows<false>(pl, slot, st, x);
     }
 
-    // The tile's (A, H) of one channel.  Without borders in the tile no map is constant, and the guard
-    // against an overflowed A times 0 is needed only if a NaN came out.  The products of four runs fit
-    // fp32 (16 coefficients), the tile's is taken in fp64.
+    // (A, H) of consecutive runs.  Without borders in the tile no map is constant, and the guard against
+    // an overflowed A times 0 is needed only if a NaN comes out.  The products of four runs stay in fp32
+    // (16 coefficients), longer ones are taken in fp64.
     template <bool GUARD>
-    __device__ __forceinline__ void tile_map(int buf, int place, double &ta, A &th) const
+    static __device__ __forceinline__ void compose(const A (&a)[P::RQ], const A (&h)[P::RQ], double &ta, A &th)
     {
-        ta = 1.0;
-        th = A(0);
-        for (int q = 0; q < P::NR; q += 8) {
-            A a[8], h[8];
+        th = h[0];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (q + k < P::NR) {
-                    a[k] = sm.mapA[buf][q + k][place];
-                    h[k] = sm.mapH[buf][q + k][place];
-                }
+        for (int k = 1; k < P::RQ; ++k)
+            th = GUARD ? apply(a[k], th, h[k]) : fma_of(a[k], th, h[k]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (q + k < P::NR)
-                    th = GUARD ? apply(a[k], th, h[k]) : fma_of(a[k], th, h[k]);
+        for (int k = 0; k < P::RQ; k += 4) {
+            A m = a[k];
 #pragma unroll
-            for (int k = 0; k < 8; k += 4)
-                if (q + k < P::NR) {
-                    if constexpr (GUARD)
-                        ta = product((double)product(product(a[k + 3], a[k + 2]), product(a[k + 1], a[k])), ta);
-                    else
-                        ta *= (double)((a[k + 3] * a[k + 2]) * (a[k + 1] * a[k]));
-                }
+            for (int e = 1; e < 4; ++e)
+                if (k + e < P::RQ)
+                    m = GUARD ? product(a[k + e], m) : a[k + e] * m;
+            if constexpr (GUARD)
+                ta = k ? product((double)m, ta) : (double)m;
+            else
+                ta = k ? (double)m * ta : (double)m;
         }
-        ta = is_const(ta) && GUARD ? ta : ta + 0.0;
+        if constexpr (!GUARD)
+            ta += 0.0;                                     // -0 marks a constant map
     }
     // Every run gets the state that enters it.
     template <bool GUARD>
-    __device__ __forceinline__ A enter_runs(int buf, int place, A x)
+    __device__ __forceinline__ void enter_runs(int buf, int r0, int at, const A (&a)[P::RQ], const A (&h)[P::RQ], A x)
     {
-        for (int q = 0; q < P::NR; q += 8) {
-            A a[8], h[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (q + k < P::NR) {
-                    a[k] = sm.mapA[buf][q + k][place];
-                    h[k] = sm.mapH[buf][q + k][place];
-                }
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (q + k < P::NR) {
-                    sm.mapH[buf][q + k][place] = x;
-                    x = GUARD ? apply(a[k], x, h[k]) : fma_of(a[k], x, h[k]);
-                }
+        for (int k = 0; k < P::RQ; ++k) {
+            sm.mapH[buf][r0 + k][at] = x;
+            x = GUARD ? apply(a[k], x, h[k]) : fma_of(a[k], x, h[k]);
         }
-        return x;
     }
 
-    // one channel of a tile: publish, find the state that enters, hand it to the runs
-    __device__ __forceinline__ void scan(const TilePlan &pl, int slot, int buf, int place)
+    // 8 channels of a tile by a warp: publish, find the state that enters, hand it to the runs
+    __device__ __forceinline__ void scan(const TilePlan &pl, int slot, int buf, int sw)
     {
         using Wd = Words<A>;
+        const unsigned all = 0xffffffffu;
+        const int q = lane >> 3, place = sw * 8 + l8, at = place ^ turn(q), r0 = q * P::RQ;
         const int64_t ch = (int64_t)pl.cb * P::W + chan_at(place);
-        if (ch >= g.n_chan)
-            return;
+        const bool real = ch < g.n_chan;
+        A a[P::RQ], h[P::RQ], th, x = A(0);
         double ta;
-        A th, x = A(0);
-        if (pl.seg)
-            tile_map<true>(buf, place, ta, th);
-        else {
-            tile_map<false>(buf, place, ta, th);
-            if (!(th == th))
-                tile_map<true>(buf, place, ta, th);
+#pragma unroll
+        for (int k = 0; k < P::RQ; ++k) {
+            a[k] = sm.mapA[buf][r0 + k][at];
+            h[k] = sm.mapH[buf][r0 + k][at];
         }
+        if (pl.seg)
+            compose<true>(a, h, ta, th);
+        else {
+            compose<false>(a, h, ta, th);
+            if (!(th == th))
+                compose<true>(a, h, ta, th);
+        }
+        const bool plain = !pl.seg && __all_sync(all, isfinite(ta) || !real);
+        // over the quarters; (pa, ph): the quarters in front
+#pragma unroll
+        for (int d = 8; d < 32; d *= 2) {
+            const double oa = __shfl_up_sync(all, ta, d);
+            const A oh = __shfl_up_sync(all, th, d);
+            if (lane >= d) {
+                th = apply_wide(ta, oh, th);
+                ta = product(ta, oa);
+            }
+        }
+        const double pa = __shfl_up_sync(all, ta, 8);
+        const A ph = __shfl_up_sync(all, th, 8);
         if (g.n_chunks > 1) {
-            ta = Wd::round_a(ta);
-            const int64_t at = (int64_t)pl.chunk * g.n_chan + ch;
+            ta = Wd::round_a(__shfl_sync(all, ta, 24 + l8));
+            th = __shfl_sync(all, th, 24 + l8);
+            const int64_t cell = (int64_t)pl.chunk * g.n_chan + ch;
             typename Wd::Inc *inc = (typename Wd::Inc *)g.inc;
             const bool first = pl.chunk == 0, fixed = first || is_const(ta);
-            if (pl.chunk + 1 < g.n_chunks) {
+            const bool publish = q == 3 && real && pl.chunk + 1 < g.n_chunks;
+            if (publish) {
                 if (fixed)
-                    st_word(inc + at, Wd::inc_bits(th));
+                    st_word(inc + cell, Wd::inc_bits(th));
                 else
-                    Wd::put(g.agg + at * Wd::N, ta, th);
+                    Wd::put(g.agg + cell * Wd::N, ta, th);
             }
             // a border (or a row outside) at the first position: nothing enters
             if (!first && !(pl.seg && (pl.lo > 0 || pl.hi == 0 || sm.begin[slot][0] >= 0))) {
-                x = state_before<A>(pl.chunk, g.n_chan, ch, g.agg, inc);
-                if (!fixed && pl.chunk + 1 < g.n_chunks)
-                    st_word(inc + at, Wd::inc_bits(apply_wide(ta, x, th)));
+                x = state_before<A>(pl.chunk, g.n_chan, ch, real, lane, g.agg, inc);
+                if (publish && !fixed)
+                    st_word(inc + cell, Wd::inc_bits(apply_wide(ta, x, th)));
             }
         }
-        // The guard is needed with constant maps, and where a run's A overflowed, which leaves the tile's
+        if (q > 0)
+            x = apply_wide(pa, x, ph);
+        // The guard is needed with constant maps, and where a run's A overflowed, which leaves its quarter's
         // not finite.
-        if (pl.seg || !isfinite(ta))
-            enter_runs<true>(buf, place, x);
+        if (plain)
+            enter_runs<false>(buf, r0, at, a, h, x);
         else
-            enter_runs<false>(buf, place, x);
+            enter_runs<true>(buf, r0, at, a, h, x);
     }
 
     // the plan warp: the next tile, and where sequences begin and end in it
@@ -803,14 +848,12 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
                     for (int64_t c = r.tid; c < g.n_chan; c += P::NC)
                         g.leave[s * g.n_chan + c] = g.enter ? g.enter[s * g.n_chan + c] : A(0);
     } else if (r.tid < P::NC + P::NSCAN) {                 // scan warps
-        const int c = r.tid - P::NC;
         int slot = 0, buf = 0;
         for (;;) {
             bar_sync(BAR_P1 + buf, P::NC + P::NSCAN);
             if (sm.plan[slot].tile < 0)
                 break;
-            if (c < P::W)
-                r.scan(sm.plan[slot], slot, buf, c);
+            r.scan(sm.plan[slot], slot, buf, r.warp - P::NW);
             __syncwarp();
             bar_arrive(BAR_P2 + buf, P::NC + P::NSCAN);
             slot = slot + 1 == NP ? 0 : slot + 1;
