@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "seq_rows.cuh"
 
@@ -11,162 +12,610 @@ namespace sla {
 namespace {
 
 constexpr int MAX_EXPERTS = 4096;
-constexpr int RT = 128;
 
 // ------------------------------------------------------------------ sort
+// A stable counting sort.  A block takes its run of entries in tiles; in a tile warp w owns 32 IT
+// consecutive entries and counts them by expert in cnt[w][.] as it goes: equal experts among 32 lanes are
+// ranked by lane (match), so an entry's rank within its warp and expert follows the order of the numbers.
+// Prefix sums over the warps, the tiles and (k_route_place) the blocks turn ranks into slots.
+//
+// Up to one tile of entries (8192 at 256 experts) one block does all of it in one launch.  Above, blocks rank
+// their runs and leave histograms, and a second launch adds what lies in front: two launches of up
+// to 148 blocks, each a pass over the ids.
+constexpr int ST = 1024;                      // threads at most
+constexpr int IT = 8;                         // entries of a lane in a tile
+
 template <typename I>
-__device__ __forceinline__ int expert_of(const I *ids, int64_t e, int n_experts)
+__device__ __forceinline__ int expert_of(I v, int n_experts)
 {
-    const I v = ids[e];
     return v >= 0 && v < (I)n_experts ? (int)v : -1;
 }
 
-// One block.  Warp w owns a contiguous run of entries; cnt[w][x] is first its number of entries of
-// expert x, then the slot its next entry of x gets.  Equal experts among a warp's 32 entries are
-// ranked by lane, so the order within an expert is the order of the entries' numbers.
-template <typename I>
-__global__ void __launch_bounds__(1024)
-    k_route_sort_one(int64_t n, int n_experts, int align, const I *ids, int64_t n_slots, int32_t *offsets,
-                     int32_t *counts, int32_t *entry, int32_t *slot)
+// off[0 .. n] = exclusive sums of cnt rounded up to `align` (all threads of the block)
+__device__ __forceinline__ void padded_offsets(int n, int align, const int *cnt, int *off)
 {
-    extern __shared__ int cnt[];
-    __shared__ int s_total;
-    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < warps * n_experts; i += blockDim.x)
-        cnt[i] = 0;
-    for (int64_t i = threadIdx.x; i < n_slots; i += blockDim.x)
-        entry[i] = -1;
-    __syncthreads();
-    const int64_t per = ((n + warps - 1) / warps + 31) / 32 * 32;
-    const int64_t e0 = min(n, per * warp), e1 = min(n, e0 + per);
-    for (int64_t e = e0 + lane; e < e1; e += 32) {
-        const int x = expert_of(ids, e, n_experts);
-        if (x >= 0)
-            atomicAdd(&cnt[warp * n_experts + x], 1);
+    __shared__ int s_warp[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int per = (n + blockDim.x - 1) / blockDim.x, e0 = min(n, (int)threadIdx.x * per), e1 = min(n, e0 + per);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e)
+        sum += (cnt[e] + align - 1) / align * align;
+    int inc = sum;
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d)
+            inc += o;
     }
+    if (lane == 31)
+        s_warp[warp] = inc;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        int at = 0;
-        for (int x = 0; x < n_experts; ++x) {
-            offsets[x] = at;
-            int next = at;
-            for (int w = 0; w < warps; ++w) {
-                const int c = cnt[w * n_experts + x];
-                cnt[w * n_experts + x] = next;
-                next += c;
-            }
-            counts[x] = next - at;
-            at += (next - at + align - 1) / align * align;
+    if (warp == 0) {
+        int w = lane < warps ? s_warp[lane] : 0;
+        for (int d = 1; d < 32; d *= 2) {
+            const int o = __shfl_up_sync(0xffffffffu, w, d);
+            if (lane >= d)
+                w += o;
         }
-        offsets[n_experts] = at;
-        s_total = at;
+        s_warp[lane] = w;
     }
     __syncthreads();
-    for (int64_t e = e0; e < e1; e += 32) {
-        const int x = e + lane < e1 ? expert_of(ids, e + lane, n_experts) : -2;
-        const unsigned peers = __match_any_sync(0xffffffffu, x);
-        if (x >= 0) {
-            const int rank = __popc(peers & ((1u << lane) - 1));
-            const int p = cnt[warp * n_experts + x] + rank;
-            slot[e + lane] = p;
-            entry[p] = (int)(e + lane);
-        } else if (x == -1)
-            slot[e + lane] = -1;
-        __syncwarp();
-        if (x >= 0 && (peers >> lane) == 1)   // the last of its kind in the warp
-            cnt[warp * n_experts + x] += __popc(peers);
-        __syncwarp();
+    int at = inc - sum + (warp ? s_warp[warp - 1] : 0);
+    for (int e = e0; e < e1; ++e) {
+        off[e] = at;
+        at += (cnt[e] + align - 1) / align * align;
     }
+    if (e1 == n && (e0 < n || threadIdx.x == 0))
+        off[n] = at;
+    __syncthreads();
+}
+
+// offsets, counts and the -1 of slots without an entry, shared out over `parts` blocks
+__device__ __forceinline__ void write_plan(int n_experts, int64_t n_slots, const int *cnt, const int *off, int part,
+                                           int parts, int32_t *offsets, int32_t *counts, int32_t *entry)
+{
+    if (part == 0) {
+        for (int e = threadIdx.x; e <= n_experts; e += blockDim.x)
+            offsets[e] = off[e];
+        for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
+            counts[e] = cnt[e];
+    }
+    const int warps = parts * (blockDim.x >> 5), lane = threadIdx.x & 31;
+    for (int e = part * (blockDim.x >> 5) + (threadIdx.x >> 5); e < n_experts; e += warps)
+        for (int64_t p = (int64_t)off[e] + cnt[e] + lane; p < off[e + 1]; p += 32)
+            entry[p] = -1;
+    for (int64_t p = off[n_experts] + (int64_t)part * blockDim.x + threadIdx.x; p < n_slots; p += (int64_t)parts * blockDim.x)
+        entry[p] = -1;
+}
+
+// Shared memory: per-warp counts (16 bits: a tile has at most 8192 entries), two arrays of sums, the offsets.
+static inline int sort_warps(int n_experts) { return std::max(1, std::min(ST / 32, (128 << 10) / (2 * n_experts))); }
+static inline size_t sort_smem(int n_experts, int warps)
+{
+    return ((size_t)warps * n_experts * 2 + 15) / 16 * 16 + sizeof(int) * (3 * (size_t)n_experts + 1);
+}
+
+template <typename I, bool ALONE>
+__global__ void __launch_bounds__(ST)
+    k_route_rank(int64_t n, int64_t per_block, int n_experts, int align, const I *ids, int64_t n_slots, int32_t *offsets,
+                 int32_t *counts, int32_t *entry, int32_t *slot, int32_t *hist)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const size_t cells = (size_t)warps * n_experts;
+    uint16_t *cnt = reinterpret_cast<uint16_t *>(smem);
+    int *run = reinterpret_cast<int *>(smem + (cells * 2 + 15) / 16 * 16);   // entries of the expert in earlier tiles
+    int *sum = run + n_experts;                                             // ... up to this tile
+    int *off = sum + n_experts;
+    const int64_t b0 = min(n, per_block * blockIdx.x), b1 = min(n, b0 + per_block);
+    for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
+        run[e] = sum[e] = 0;
+    for (int64_t tile = b0; ALONE || tile < b1; tile += (int64_t)warps * 32 * IT) {
+        const int64_t e0 = tile + (int64_t)warp * 32 * IT + lane;
+        int x[IT], rank[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+            x[i] = e0 + 32 * i < b1 ? expert_of(ids[e0 + 32 * i], n_experts) : -2;
+        for (size_t i = threadIdx.x; i < (cells + 7) / 8; i += blockDim.x)
+            reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        uint16_t *mine = cnt + (size_t)warp * n_experts;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const unsigned peers = __match_any_sync(0xffffffffu, x[i]);
+            const int before = x[i] >= 0 ? mine[x[i]] : 0;
+            rank[i] = before + __popc(peers & ((1u << lane) - 1));
+            __syncwarp();
+            if (x[i] >= 0 && (peers >> lane) == 1)     // the last of its kind
+                mine[x[i]] = (uint16_t)(before + __popc(peers));
+            __syncwarp();
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < n_experts; e += blockDim.x) {
+            int acc = 0;
+#pragma unroll 8
+            for (int w = 0; w < warps; ++w) {
+                const int c = cnt[(size_t)w * n_experts + e];
+                cnt[(size_t)w * n_experts + e] = (uint16_t)acc;
+                acc += c;
+            }
+            run[e] = sum[e];
+            sum[e] += acc;
+        }
+        __syncthreads();
+        if constexpr (ALONE)
+            padded_offsets(n_experts, align, sum, off);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int64_t e = e0 + 32 * i;
+            if (x[i] >= 0) {
+                const int p = (ALONE ? off[x[i]] : run[x[i]]) + mine[x[i]] + rank[i];
+                slot[e] = p;
+                if (ALONE)
+                    entry[p] = (int)e;
+            } else if (x[i] == -1)
+                slot[e] = -1;
+        }
+        if constexpr (ALONE) {
+            write_plan(n_experts, n_slots, sum, off, 0, 1, offsets, counts, entry);
+            return;
+        }
+        __syncthreads();
+    }
+    for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
+        hist[(size_t)blockIdx.x * n_experts + e] = sum[e];
+}
+
+// Ranks within a block's run -> slots.
+template <typename I>
+__global__ void __launch_bounds__(ST)
+    k_route_place(int64_t n, int64_t per_block, int n_experts, int align, const I *ids, int64_t n_slots,
+                  int32_t *offsets, int32_t *counts, int32_t *entry, int32_t *slot, const int32_t *hist)
+{
+    extern __shared__ __align__(16) unsigned char smem[];
+    int *cnt = reinterpret_cast<int *>(smem), *base = cnt + n_experts, *off = base + n_experts;
+    const int64_t b0 = min(n, per_block * blockIdx.x), b1 = min(n, b0 + per_block);
+    // totals and what lies in front, `parts` threads an expert
+    const int parts = max(1, (int)blockDim.x / n_experts);
+    for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
+        cnt[e] = base[e] = 0;
+    __syncthreads();
+    if ((int)threadIdx.x < parts * n_experts || parts == 1)
+        for (int e = threadIdx.x % (parts == 1 ? blockDim.x : (unsigned)n_experts); e < n_experts; e += blockDim.x) {
+            const int part = parts == 1 ? 0 : threadIdx.x / n_experts;
+            int all = 0, front = 0;
+#pragma unroll 8
+            for (int g = part; g < (int)gridDim.x; g += parts) {
+                const int v = hist[(size_t)g * n_experts + e];
+                all += v;
+                front += g < (int)blockIdx.x ? v : 0;
+            }
+            atomicAdd(&cnt[e], all);                    // whole numbers: any order gives the same sums
+            atomicAdd(&base[e], front);
+        }
+    __syncthreads();
+    padded_offsets(n_experts, align, cnt, off);
+    for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
+        base[e] += off[e];
+    __syncthreads();
+    for (int64_t t = b0 + threadIdx.x; t < b1; t += (int64_t)blockDim.x * IT) {
+        int x[IT], r[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int64_t e = t + (int64_t)i * blockDim.x;
+            x[i] = e < b1 ? expert_of(ids[e], n_experts) : -1;
+            r[i] = e < b1 ? slot[e] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int64_t e = t + (int64_t)i * blockDim.x;
+            if (x[i] >= 0) {
+                const int p = base[x[i]] + r[i];
+                slot[e] = p;
+                entry[p] = (int)e;
+            }
+        }
+    }
+    write_plan(n_experts, n_slots, cnt, off, blockIdx.x, gridDim.x, offsets, counts, entry);
+}
+
+// Blocks of the two-launch sort: a tile each at least, at most 148, and histograms of 64 Ki numbers at most,
+// since every block of the second launch reads them all.
+static inline int64_t sort_blocks(int64_t n, int n_experts)
+{
+    const int64_t tile = (int64_t)sort_warps(n_experts) * 32 * IT;
+    return std::max<int64_t>(1, std::min<int64_t>({(n + tile - 1) / tile, (int64_t)148, (int64_t)65536 / n_experts}));
 }
 
 // ------------------------------------------------------------------ products
-// Rows of the slot side that belong to no entry: padding of the experts (zeros), and with `fill`
-// the slots behind the last expert's.
-template <typename S>
-__global__ void __launch_bounds__(RT) k_route_padding(int n_experts, int64_t n_slots, int64_t n_chan,
-                                                      const int32_t *offsets, const int32_t *counts, S *xs,
-                                                      int64_t ldxs, int fill)
-{
-    // experts, then the rest
-    for (int x = blockIdx.x; x <= n_experts; x += gridDim.x) {
-        int64_t r0, r1;
-        if (x < n_experts) {
-            r0 = (int64_t)offsets[x] + counts[x];
-            r1 = offsets[x + 1];
-        } else {
-            r0 = offsets[n_experts];
-            r1 = fill ? n_slots : r0;
-        }
-        r0 = max(r0, (int64_t)0);
-        r1 = min(r1, n_slots);
-        for (int64_t r = r0; r < r1; ++r)
-            for (int64_t c = threadIdx.x; c < n_chan; c += RT)
-                xs[r * ldxs + c] = S(0.0f);
+// One group of G threads a token, a row cut into units of U values (16 bytes where all rows are aligned to
+// it).  A token's row crosses memory once: read and written to each of its slots, or summed from them;
+// the gradient on the pattern is the dot product of the rows that pass anyway.  Sums run over j in
+// order and over the channels in an order fixed by n_chan and the rows' alignment, so results do not
+// depend on scheduling.
+constexpr int PT = 256;
+
+template <typename S, int U>
+struct Unit {
+    using A = typename RowType<S>::A;
+    S s[U];
+    __device__ __forceinline__ void load(const S *p)
+    {
+        if constexpr (U * sizeof(S) == 16)
+            *reinterpret_cast<uint4 *>(s) = __ldg(reinterpret_cast<const uint4 *>(p));
+        else if constexpr (U * sizeof(S) == 4 && U > 1)
+            *reinterpret_cast<unsigned *>(s) = __ldg(reinterpret_cast<const unsigned *>(p));
+        else
+            s[0] = p[0];
     }
-}
+    __device__ __forceinline__ void load(const S *p, int left)
+    {
+        if (U == 1 || left >= U)
+            load(p);
+        else if constexpr (U > 1)
+#pragma unroll
+            for (int e = 0; e < U; ++e)
+                s[e] = e < left ? p[e] : S(0.0f);
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int e = 0; e < U; ++e)
+            s[e] = S(0.0f);
+    }
+    __device__ __forceinline__ void store(S *p, int left) const
+    {
+        if (U == 1 || left >= U) {
+            if constexpr (U * sizeof(S) == 16)
+                *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(s);
+            else if constexpr (U * sizeof(S) == 4 && U > 1)
+                *reinterpret_cast<unsigned *>(p) = *reinterpret_cast<const unsigned *>(s);
+            else
+                p[0] = s[0];
+        } else if constexpr (U > 1)
+#pragma unroll
+            for (int e = 0; e < U; ++e)
+                if (e < left)
+                    p[e] = s[e];
+    }
+    __device__ __forceinline__ A up(int e) const { return RowType<S>::up(s[e]); }
+    __device__ __forceinline__ void set(int e, A v) { s[e] = RowType<S>::down(v); }
+};
 
-// R^T x: one block per token writes its row to each of its slots.
 template <typename S>
-__global__ void __launch_bounds__(RT)
-    k_route_to_slots(int64_t n_tokens, int top_k, int64_t n_slots, int64_t n_chan, const S *x, int64_t ldx,
-                     const int32_t *slot, const typename RowType<S>::A *weight, S *xs, int64_t ldxs)
-{
-    using R = RowType<S>;
-    for (int64_t t = blockIdx.x; t < n_tokens; t += gridDim.x)
-        for (int j = 0; j < top_k; ++j) {
-            const int64_t p = slot[t * top_k + j];
-            if (p < 0 || p >= n_slots)
-                continue;
-            for (int64_t c = threadIdx.x; c < n_chan; c += RT) {
-                const S v = x[t * ldx + c];
-                xs[p * ldxs + c] = weight ? R::down(weight[t * top_k + j] * R::up(v)) : v;
-            }
-        }
-}
+struct RouteArgs {
+    using A = typename RowType<S>::A;
+    int64_t n_tokens, n_slots, n_chan;
+    int top_k, n_experts, fill, fill_blocks;
+    const int32_t *offsets, *counts, *slot;
+    const A *weight;
+    const S *tok;             // token side, read: x, dy
+    const S *slt;             // slot side, read: ys, dxs
+    S *tok_out, *slt_out;
+    int64_t ldtok, ldslt, ldtok_out, ldslt_out;
+    A *dweight;
+};
 
-// R xs: one block per token sums its slots' rows.
-template <typename S>
-__global__ void __launch_bounds__(RT)
-    k_route_to_tokens(int64_t n_tokens, int top_k, int64_t n_slots, int64_t n_chan, const S *xs, int64_t ldxs,
-                      const int32_t *slot, const typename RowType<S>::A *weight, S *y, int64_t ldy)
+// Sums of K values over a group of G threads (a power of two, a warp at least), in a fixed order; valid in its
+// first thread.
+template <typename A, int K>
+__device__ __forceinline__ void group_sum(A (&d)[K], int G, A (*s_red)[K])
 {
-    using R = RowType<S>;
-    using A = typename R::A;
-    for (int64_t t = blockIdx.x; t < n_tokens; t += gridDim.x)
-        for (int64_t c = threadIdx.x; c < n_chan; c += RT) {
-            A v = A(0);
-            for (int j = 0; j < top_k; ++j) {
-                const int64_t p = slot[t * top_k + j];
-                if (p < 0 || p >= n_slots)
-                    continue;
-                const A u = R::up(xs[p * ldxs + c]);
-                v = weight ? fma_of(weight[t * top_k + j], u, v) : v + u;
-            }
-            y[t * ldy + c] = R::down(v);
-        }
-}
-
-// The gradient on the pattern: one warp per entry.
-template <typename S>
-__global__ void __launch_bounds__(RT)
-    k_route_pattern(int64_t n_tokens, int top_k, int64_t n_slots, int64_t n_chan, const S *x, int64_t ldx, const S *xs,
-                    int64_t ldxs, const int32_t *slot, typename RowType<S>::A *dweight)
-{
-    using R = RowType<S>;
-    using A = typename R::A;
-    const int lane = threadIdx.x & 31;
-    const int64_t n = n_tokens * top_k;
-    for (int64_t e = (int64_t)blockIdx.x * (RT / 32) + (threadIdx.x >> 5); e < n; e += (int64_t)gridDim.x * (RT / 32)) {
-        const int64_t p = slot[e], t = e / top_k;
-        A v = A(0);
-        if (p >= 0 && p < n_slots)
-            for (int64_t c = lane; c < n_chan; c += 32)
-                v = fma_of(R::up(x[t * ldx + c]), R::up(xs[p * ldxs + c]), v);
+#pragma unroll
+    for (int j = 0; j < K; ++j)
         for (int o = 16; o > 0; o >>= 1)
-            v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0)
-            dweight[e] = v;
+            d[j] += __shfl_xor_sync(0xffffffffu, d[j], o);
+    if (G > 32) {
+        const int warp = threadIdx.x >> 5;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                s_red[warp][j] = d[j];
+        __syncthreads();
+        if ((threadIdx.x & (G - 1)) == 0)
+#pragma unroll
+            for (int j = 0; j < K; ++j) {
+                A t = A(0);
+                for (int w = 0; w < G / 32; ++w)
+                    t += s_red[warp + w][j];
+                d[j] = t;
+            }
     }
+}
+
+// Zeros in the slots without an entry, a row a warp: block f of the fill blocks takes the padding rows r of
+// expert e with (e + r) % fill_blocks = f, and its share of the rest.
+template <typename S, int U>
+__device__ __forceinline__ void fill_blanks(const RouteArgs<S> &g, int f)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nf = g.fill_blocks;
+    const int64_t nunits = (g.n_chan + U - 1) / U;
+    Unit<S, U> z;
+    z.zero();
+    auto clear = [&](int64_t row) {
+        S *p = g.slt_out + row * g.ldslt_out;
+        for (int64_t u = lane; u < nunits; u += 32)
+            z.store(p + u * U, (int)min((int64_t)U, g.n_chan - u * U));
+    };
+    for (int e0 = warp * 32; e0 < g.n_experts; e0 += PT) {
+        const int e = e0 + lane;
+        int64_t r0 = 0, n = 0;
+        if (e < g.n_experts) {
+            r0 = min(max((int64_t)g.offsets[e] + g.counts[e], (int64_t)0), g.n_slots);
+            n = min((int64_t)g.offsets[e + 1], g.n_slots) - r0;
+        }
+        const int first = (f + nf - e % nf) % nf;
+        for (unsigned has = __ballot_sync(0xffffffffu, first < n); has; has &= has - 1) {
+            const int l = __ffs(has) - 1;
+            const int64_t q0 = __shfl_sync(0xffffffffu, r0, l), m = __shfl_sync(0xffffffffu, n, l);
+            for (int64_t r = __shfl_sync(0xffffffffu, first, l); r < m; r += nf)
+                clear(q0 + r);
+        }
+    }
+    if (g.fill)
+        for (int64_t r = max((int64_t)g.offsets[g.n_experts], (int64_t)0) + (int64_t)f * (PT / 32) + warp; r < g.n_slots;
+             r += (int64_t)nf * (PT / 32))
+            clear(r);
+}
+
+// R^T x, and with dweight x . ys on the pattern.  KU choices and NV units at a time.
+template <typename S, int U, int KU, int NV>
+__global__ void __launch_bounds__(PT) k_route_to_slots(const __grid_constant__ RouteArgs<S> g, int G)
+{
+    using A = typename RowType<S>::A;
+    __shared__ A s_red[PT / 32][KU];
+    if ((int)blockIdx.x < g.fill_blocks) {
+        fill_blanks<S, U>(g, blockIdx.x);
+        return;
+    }
+    const int64_t t = (int64_t)(blockIdx.x - g.fill_blocks) * (PT / G) + threadIdx.x / G;
+    const int lane = threadIdx.x & (G - 1);
+    const bool live = t < g.n_tokens;
+    const int nunits = live ? (int)((g.n_chan + U - 1) / U) : 0;
+    const S *x = g.tok + (live ? t : 0) * g.ldtok;
+    for (int j0 = 0; j0 < g.top_k; j0 += KU) {
+        int64_t p[KU];
+        A w[KU], dot[KU];
+#pragma unroll
+        for (int j = 0; j < KU; ++j) {
+            const bool has = live && j0 + j < g.top_k;
+            p[j] = has ? g.slot[t * g.top_k + j0 + j] : -1;
+            if (p[j] >= g.n_slots)
+                p[j] = -1;
+            w[j] = has && g.weight ? g.weight[t * g.top_k + j0 + j] : A(1);
+            dot[j] = A(0);
+        }
+        for (int u0 = lane; u0 < nunits; u0 += G * NV) {
+            Unit<S, U> v[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t c = (int64_t)(u0 + i * G) * U;
+                if (u0 + i * G < nunits)
+                    v[i].load(x + c, (int)min((int64_t)U, g.n_chan - c));
+                else
+                    v[i].zero();
+            }
+            if (g.dweight) {
+#pragma unroll
+                for (int j = 0; j < KU; ++j) {
+                    if (p[j] < 0)
+                        continue;
+                    const S *y = g.slt + p[j] * g.ldslt;
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        const int64_t c = (int64_t)(u0 + i * G) * U;
+                        if (u0 + i * G >= nunits)
+                            continue;
+                        Unit<S, U> o;
+                        o.load(y + c, (int)min((int64_t)U, g.n_chan - c));
+#pragma unroll
+                        for (int e = 0; e < U; ++e)
+                            dot[j] = fma_of(v[i].up(e), o.up(e), dot[j]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < KU; ++j) {
+                if (p[j] < 0)
+                    continue;
+                S *to = g.slt_out + p[j] * g.ldslt_out;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int64_t c = (int64_t)(u0 + i * G) * U;
+                    if (u0 + i * G >= nunits)
+                        continue;
+                    Unit<S, U> o = v[i];
+                    if (g.weight)
+#pragma unroll
+                        for (int e = 0; e < U; ++e)
+                            o.set(e, w[j] * v[i].up(e));
+                    o.store(to + c, (int)min((int64_t)U, g.n_chan - c));
+                }
+            }
+        }
+        if (g.dweight) {
+            group_sum<A, KU>(dot, G, s_red);
+            if (lane == 0 && live)
+#pragma unroll
+                for (int j = 0; j < KU; ++j)
+                    if (j0 + j < g.top_k)
+                        g.dweight[t * g.top_k + j0 + j] = dot[j];
+        }
+    }
+}
+
+// R ys, and with dweight x . ys on the pattern.
+template <typename S, int U, int KU, int NV>
+__global__ void __launch_bounds__(PT) k_route_to_tokens(const __grid_constant__ RouteArgs<S> g, int G)
+{
+    using A = typename RowType<S>::A;
+    __shared__ A s_red[PT / 32][KU];
+    const int64_t t = (int64_t)blockIdx.x * (PT / G) + threadIdx.x / G;
+    const int lane = threadIdx.x & (G - 1);
+    const bool live = t < g.n_tokens;
+    const int nunits = live ? (int)((g.n_chan + U - 1) / U) : 0;
+    const bool one = g.top_k <= KU;            // all choices at once: the dot products pass with the sum
+    int64_t p[KU];
+    A w[KU], dot[KU];
+    auto choices = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < KU; ++j) {
+            const bool has = live && j0 + j < g.top_k;
+            p[j] = has ? g.slot[t * g.top_k + j0 + j] : -1;
+            if (p[j] >= g.n_slots)
+                p[j] = -1;
+            w[j] = has && g.weight ? g.weight[t * g.top_k + j0 + j] : A(1);
+        }
+    };
+    const S *x = g.dweight ? g.tok + (live ? t : 0) * g.ldtok : nullptr;
+    choices(0);
+#pragma unroll
+    for (int j = 0; j < KU; ++j)
+        dot[j] = A(0);
+    for (int u0 = lane; u0 < nunits; u0 += G * NV) {
+        A acc[NV][U];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < U; ++e)
+                acc[i][e] = A(0);
+        for (int j0 = 0; j0 < g.top_k; j0 += KU) {
+            if (!one)
+                choices(j0);
+            Unit<S, U> o[KU][NV];
+#pragma unroll
+            for (int j = 0; j < KU; ++j)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int64_t c = (int64_t)(u0 + i * G) * U;
+                    if (p[j] >= 0 && u0 + i * G < nunits)
+                        o[j][i].load(g.slt + p[j] * g.ldslt + c, (int)min((int64_t)U, g.n_chan - c));
+                    else
+                        o[j][i].zero();
+                }
+            if (one && x) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int64_t c = (int64_t)(u0 + i * G) * U;
+                    if (u0 + i * G >= nunits)
+                        continue;
+                    Unit<S, U> v;
+                    v.load(x + c, (int)min((int64_t)U, g.n_chan - c));
+#pragma unroll
+                    for (int j = 0; j < KU; ++j)
+                        if (p[j] >= 0)
+#pragma unroll
+                            for (int e = 0; e < U; ++e)
+                                dot[j] = fma_of(v.up(e), o[j][i].up(e), dot[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < KU; ++j)
+                if (p[j] >= 0)
+#pragma unroll
+                    for (int i = 0; i < NV; ++i)
+#pragma unroll
+                        for (int e = 0; e < U; ++e)
+                            acc[i][e] = fma_of(w[j], o[j][i].up(e), acc[i][e]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t c = (int64_t)(u0 + i * G) * U;
+            if (u0 + i * G >= nunits)
+                continue;
+            Unit<S, U> o;
+#pragma unroll
+            for (int e = 0; e < U; ++e)
+                o.set(e, acc[i][e]);
+            o.store(g.tok_out + t * g.ldtok_out + c, (int)min((int64_t)U, g.n_chan - c));
+        }
+    }
+    if (!g.dweight)
+        return;
+    for (int j0 = 0; j0 < g.top_k; j0 += KU) {
+        if (!one) {
+            choices(j0);
+#pragma unroll
+            for (int j = 0; j < KU; ++j)
+                dot[j] = A(0);
+            for (int u = lane; u < nunits; u += G) {
+                const int64_t c = (int64_t)u * U;
+                Unit<S, U> v, o;
+                v.load(x + c, (int)min((int64_t)U, g.n_chan - c));
+#pragma unroll
+                for (int j = 0; j < KU; ++j)
+                    if (p[j] >= 0) {
+                        o.load(g.slt + p[j] * g.ldslt + c, (int)min((int64_t)U, g.n_chan - c));
+#pragma unroll
+                        for (int e = 0; e < U; ++e)
+                            dot[j] = fma_of(v.up(e), o.up(e), dot[j]);
+                    }
+            }
+        }
+        group_sum<A, KU>(dot, G, s_red);
+        if (lane == 0 && live)
+#pragma unroll
+            for (int j = 0; j < KU; ++j)
+                if (j0 + j < g.top_k)
+                    g.dweight[t * g.top_k + j0 + j] = dot[j];
+    }
+}
+
+// Threads a token: its units shared out NV each, a warp at least, a block at most.
+static inline int group_of(int64_t n_chan, int U, int NV)
+{
+    const int64_t want = (n_chan + (int64_t)U * NV - 1) / ((int64_t)U * NV);
+    int G = 32;
+    while (G < PT && G < want)
+        G *= 2;
+    return G;
+}
+
+template <typename S, int U, int KU, int NV>
+sla_status launch_product(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
+{
+    const int G = group_of(g.n_chan, U, NV);
+    const int64_t blocks = (g.n_tokens + PT / G - 1) / (PT / G);
+    if (to_slots) {
+        // a fill block for every 64 KiB of slot rows that may be blank, at most two an SM
+        const int64_t bytes = g.n_slots * g.n_chan * (int64_t)sizeof(S);
+        g.fill_blocks = (int)std::max<int64_t>(1, std::min<int64_t>(296, bytes >> 16));
+        k_route_to_slots<S, U, KU, NV><<<(unsigned)(blocks + g.fill_blocks), PT, 0, s>>>(g, G);
+    } else if (blocks > 0)
+        k_route_to_tokens<S, U, KU, NV><<<(unsigned)blocks, PT, 0, s>>>(g, G);
+    SLA_CUDA_TRY(cudaGetLastError());
+    return SLA_SUCCESS;
+}
+
+// About 8 loads in flight a thread: KU choices times NV units (fp64 and short units alike).
+template <typename S, int U>
+sla_status launch_unit(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
+{
+    if (g.top_k <= 2)
+        return launch_product<S, U, 2, 4>(g, to_slots, s);
+    if (g.top_k <= 4)
+        return launch_product<S, U, 4, 2>(g, to_slots, s);
+    return launch_product<S, U, 8, 1>(g, to_slots, s);
+}
+
+template <typename S>
+sla_status run_product(RouteArgs<S> g, bool to_slots, cudaStream_t s)
+{
+    uintptr_t bits = 0;
+    auto see = [&](const void *p, int64_t ld) {
+        if (p)
+            bits |= (uintptr_t)p | (uintptr_t)(ld * (int64_t)sizeof(S));
+    };
+    see(g.tok, g.ldtok);
+    see(g.slt, g.ldslt);
+    see(g.tok_out, g.ldtok_out);
+    see(g.slt_out, g.ldslt_out);
+    if (bits % 16 == 0)
+        return launch_unit<S, 16 / (int)sizeof(S)>(g, to_slots, s);
+    if constexpr (sizeof(S) == 2)
+        if (bits % 4 == 0)
+            return launch_unit<S, 2>(g, to_slots, s);
+    return launch_unit<S, 1>(g, to_slots, s);
 }
 
 sla_status check_route(int32_t dtype, int64_t n_tokens, int32_t top_k, int64_t n_slots, int64_t n_chan,
@@ -201,8 +650,6 @@ sla_status check_plan(int32_t n_experts, const int32_t *d_offsets, const int32_t
     return SLA_SUCCESS;
 }
 
-unsigned blocks_for(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>(n, 1 << 20)); }
-
 }  // namespace
 }  // namespace sla
 
@@ -212,10 +659,10 @@ extern "C" {
 
 size_t sla_route_workspace_bytes(int64_t n_tokens, int32_t top_k, int32_t n_experts)
 {
-    (void)n_tokens;
-    (void)top_k;
-    (void)n_experts;
-    return 0;
+    if (n_tokens <= 0 || top_k < 1 || n_tokens > INT32_MAX / top_k || n_experts < 1 || n_experts > MAX_EXPERTS)
+        return 0;
+    const int64_t blocks = sort_blocks(n_tokens * top_k, n_experts);
+    return blocks > 1 ? sizeof(int32_t) * (size_t)blocks * (size_t)n_experts : 0;
 }
 
 sla_status sla_route_sort(int64_t n_tokens, int32_t top_k, int32_t n_experts, int32_t align, const void *d_expert,
@@ -235,19 +682,42 @@ sla_status sla_route_sort(int64_t n_tokens, int32_t top_k, int32_t n_experts, in
         return fail(SLA_ERR_INVALID_ARG, "n_slots must be at least n_tokens * top_k + n_experts * (align - 1), below 2^31");
     if (!d_offsets || !d_counts || (n > 0 && (!d_expert || !d_slot)) || (n_slots > 0 && !d_entry))
         return fail(SLA_ERR_INVALID_ARG, "NULL array");
-    if (work_bytes < sla_route_workspace_bytes(n_tokens, top_k, n_experts))
-        return fail(SLA_ERR_INVALID_ARG, "d_work is too small");
+    const size_t need = sla_route_workspace_bytes(n_tokens, top_k, n_experts);
+    if (need && (!d_work || work_bytes < need || (uintptr_t)d_work % 16))
+        return fail(SLA_ERR_INVALID_ARG, "d_work is NULL, smaller than sla_route_workspace_bytes or not 16-byte aligned");
     cudaStream_t s = (cudaStream_t)stream;
-    const int warps = std::max(1, std::min(32, (128 << 10) / (4 * n_experts)));
-    const size_t smem = sizeof(int) * (size_t)warps * n_experts;
-    auto launch = [&](auto kernel, auto ids) -> sla_status {
-        SLA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 << 10));
-        kernel<<<1, 32 * warps, smem, s>>>(n, n_experts, align, ids, n_slots, d_offsets, d_counts, d_entry, d_slot);
+    const int warps = sort_warps(n_experts);
+    const size_t smem = sort_smem(n_experts, warps);
+    // with few entries only the warps that have some
+    const int64_t blocks = sort_blocks(n, n_experts);
+    auto allow = [&](auto kernel) -> sla_status {
+        if (smem > 48 << 10)
+            SLA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        return SLA_SUCCESS;
+    };
+    auto run = [&](auto ids) -> sla_status {
+        using I = std::remove_const_t<std::remove_pointer_t<decltype(ids)>>;
+        if (blocks == 1) {
+            const int w = (int)std::min<int64_t>(warps, std::max<int64_t>({1, (n + 32 * IT - 1) / (32 * IT),
+                                                                          ((int64_t)n_experts + 127) / 128}));
+            SLA_TRY(allow(k_route_rank<I, true>));
+            k_route_rank<I, true><<<1, 32 * w, smem, s>>>(n, n, n_experts, align, ids, n_slots, d_offsets, d_counts,
+                                                         d_entry, d_slot, nullptr);
+        } else {
+            const int64_t tile = (int64_t)warps * 32 * IT, per = ((n + blocks - 1) / blocks + tile - 1) / tile * tile;
+            const unsigned grid = (unsigned)((n + per - 1) / per);
+            SLA_TRY(allow(k_route_rank<I, false>));
+            k_route_rank<I, false><<<grid, 32 * warps, smem, s>>>(n, per, n_experts, align, ids, n_slots, d_offsets,
+                                                                 d_counts, d_entry, d_slot, (int32_t *)d_work);
+            const size_t smem2 = sizeof(int) * (3 * (size_t)n_experts + 1);
+            SLA_TRY(allow(k_route_place<I>));
+            k_route_place<I><<<grid, ST, smem2, s>>>(n, per, n_experts, align, ids, n_slots, d_offsets, d_counts,
+                                                     d_entry, d_slot, (const int32_t *)d_work);
+        }
         SLA_CUDA_TRY(cudaGetLastError());
         return SLA_SUCCESS;
     };
-    return id_bytes == 4 ? launch(k_route_sort_one<int32_t>, (const int32_t *)d_expert)
-                         : launch(k_route_sort_one<int64_t>, (const int64_t *)d_expert);
+    return id_bytes == 4 ? run((const int32_t *)d_expert) : run((const int64_t *)d_expert);
 }
 
 sla_status sla_route_dispatch(int32_t dtype, int64_t n_tokens, int32_t top_k, int32_t n_experts, int64_t n_slots,
@@ -279,18 +749,26 @@ sla_status sla_route_dispatch_adjoint(int32_t dtype, int64_t n_tokens, int32_t t
     SLA_TRY(check_rows(d_dx, lddx, n_tokens, n_chan, true));
     if (d_dweight)
         SLA_TRY(check_rows(d_x, ldx, n_tokens, n_chan, false));
-    cudaStream_t s = (cudaStream_t)stream;
     return with_row_type(dtype, [&](auto tag) {
         using S = decltype(tag);
         using A = typename RowType<S>::A;
-        k_route_to_tokens<S><<<blocks_for(n_tokens), RT, 0, s>>>(n_tokens, top_k, n_slots, n_chan, (const S *)d_dxs,
-                                                                 lddxs, d_slot, (const A *)d_weight, (S *)d_dx, lddx);
-        if (d_dweight)
-            k_route_pattern<S><<<blocks_for(n_tokens), RT, 0, s>>>(n_tokens, top_k, n_slots, n_chan, (const S *)d_x,
-                                                                   ldx, (const S *)d_dxs, lddxs, d_slot,
-                                                                   (A *)d_dweight);
-        SLA_CUDA_TRY(cudaGetLastError());
-        return (sla_status)SLA_SUCCESS;
+        RouteArgs<S> g{};
+        g.n_tokens = n_tokens;
+        g.n_slots = n_slots;
+        g.n_chan = n_chan;
+        g.top_k = top_k;
+        g.slot = d_slot;
+        g.weight = (const A *)d_weight;
+        g.slt = (const S *)d_dxs;
+        g.ldslt = lddxs;
+        g.tok_out = (S *)d_dx;
+        g.ldtok_out = lddx;
+        if (d_dweight) {
+            g.tok = (const S *)d_x;
+            g.ldtok = ldx;
+            g.dweight = (A *)d_dweight;
+        }
+        return run_product<S>(g, false, (cudaStream_t)stream);
     });
 }
 
@@ -308,22 +786,30 @@ sla_status sla_route_combine_adjoint(int32_t dtype, int64_t n_tokens, int32_t to
     SLA_TRY(check_rows(d_dys, lddys, n_slots, n_chan, true));
     if (d_dweight && n_tokens > 0)
         SLA_TRY(check_rows(d_ys, ldys, n_slots, n_chan, false));
-    cudaStream_t s = (cudaStream_t)stream;
     return with_row_type(dtype, [&](auto tag) {
         using S = decltype(tag);
         using A = typename RowType<S>::A;
-        k_route_padding<S><<<blocks_for(n_experts + 1), RT, 0, s>>>(n_experts, n_slots, n_chan, d_offsets, d_counts,
-                                                                    (S *)d_dys, lddys, (flags & SLA_FILL_REST) != 0);
-        if (n_tokens > 0)
-            k_route_to_slots<S><<<blocks_for(n_tokens), RT, 0, s>>>(n_tokens, top_k, n_slots, n_chan, (const S *)d_dy,
-                                                                    lddy, d_slot, (const A *)d_weight, (S *)d_dys,
-                                                                    lddys);
-        if (d_dweight && n_tokens > 0)
-            k_route_pattern<S><<<blocks_for(n_tokens), RT, 0, s>>>(n_tokens, top_k, n_slots, n_chan, (const S *)d_dy,
-                                                                   lddy, (const S *)d_ys, ldys, d_slot,
-                                                                   (A *)d_dweight);
-        SLA_CUDA_TRY(cudaGetLastError());
-        return (sla_status)SLA_SUCCESS;
+        RouteArgs<S> g{};
+        g.n_tokens = n_tokens;
+        g.n_slots = n_slots;
+        g.n_chan = n_chan;
+        g.top_k = top_k;
+        g.n_experts = n_experts;
+        g.fill = (flags & SLA_FILL_REST) != 0;
+        g.offsets = d_offsets;
+        g.counts = d_counts;
+        g.slot = d_slot;
+        g.weight = (const A *)d_weight;
+        g.tok = (const S *)d_dy;
+        g.ldtok = lddy;
+        g.slt_out = (S *)d_dys;
+        g.ldslt_out = lddys;
+        if (d_dweight && n_tokens > 0) {
+            g.slt = (const S *)d_ys;
+            g.ldslt = ldys;
+            g.dweight = (A *)d_dweight;
+        }
+        return run_product<S>(g, true, (cudaStream_t)stream);
     });
 }
 
