@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(ST)
     const int64_t b0 = min(n, per_block * blockIdx.x), b1 = min(n, b0 + per_block);
     for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
         run[e] = sum[e] = 0;
-    for (int64_t tile = b0; ALONE || tile < b1; tile += (int64_t)warps * 32 * IT) {
+    for (int64_t tile = b0; tile < b1 || (ALONE && tile == b0); tile += (int64_t)warps * 32 * IT) {
         const int64_t e0 = tile + (int64_t)warp * 32 * IT + lane;
         int x[IT], rank[IT];
 #pragma unroll
@@ -155,14 +155,13 @@ __global__ void __launch_bounds__(ST)
             } else if (x[i] == -1)
                 slot[e] = -1;
         }
-        if constexpr (ALONE) {
-            write_plan(n_experts, n_slots, sum, off, 0, 1, offsets, counts, entry);
-            return;
-        }
         __syncthreads();
     }
-    for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
-        hist[(size_t)blockIdx.x * n_experts + e] = sum[e];
+    if constexpr (ALONE)
+        write_plan(n_experts, n_slots, sum, off, 0, 1, offsets, counts, entry);
+    else
+        for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
+            hist[(size_t)blockIdx.x * n_experts + e] = sum[e];
 }
 
 // Ranks within a block's run -> slots.
@@ -237,48 +236,60 @@ constexpr int PT = 256;
 template <typename S, int U>
 struct Unit {
     using A = typename RowType<S>::A;
-    S s[U];
-    __device__ __forceinline__ void load(const S *p)
-    {
-        if constexpr (U * sizeof(S) == 16)
-            *reinterpret_cast<uint4 *>(s) = __ldg(reinterpret_cast<const uint4 *>(p));
-        else if constexpr (U * sizeof(S) == 4 && U > 1)
-            *reinterpret_cast<unsigned *>(s) = __ldg(reinterpret_cast<const unsigned *>(p));
-        else
-            s[0] = p[0];
-    }
+    static constexpr int BYTES = U * (int)sizeof(S);
+    using Raw = std::conditional_t<BYTES == 16, uint4,
+                                   std::conditional_t<BYTES == 8, uint2, std::conditional_t<BYTES == 4, unsigned, uint16_t>>>;
+    Raw raw;
     __device__ __forceinline__ void load(const S *p, int left)
     {
         if (U == 1 || left >= U)
-            load(p);
-        else if constexpr (U > 1)
+            raw = __ldg(reinterpret_cast<const Raw *>(p));
+        else if constexpr (U > 1) {
+            S s[U];
 #pragma unroll
             for (int e = 0; e < U; ++e)
                 s[e] = e < left ? p[e] : S(0.0f);
-    }
-    __device__ __forceinline__ void zero()
-    {
-#pragma unroll
-        for (int e = 0; e < U; ++e)
-            s[e] = S(0.0f);
+            memcpy(&raw, s, BYTES);
+        }
     }
     __device__ __forceinline__ void store(S *p, int left) const
     {
-        if (U == 1 || left >= U) {
-            if constexpr (U * sizeof(S) == 16)
-                *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(s);
-            else if constexpr (U * sizeof(S) == 4 && U > 1)
-                *reinterpret_cast<unsigned *>(p) = *reinterpret_cast<const unsigned *>(s);
-            else
-                p[0] = s[0];
-        } else if constexpr (U > 1)
+        if (U == 1 || left >= U)
+            *reinterpret_cast<Raw *>(p) = raw;
+        else if constexpr (U > 1) {
+            S s[U];
+            memcpy(s, &raw, BYTES);
 #pragma unroll
             for (int e = 0; e < U; ++e)
                 if (e < left)
                     p[e] = s[e];
+        }
     }
-    __device__ __forceinline__ A up(int e) const { return RowType<S>::up(s[e]); }
-    __device__ __forceinline__ void set(int e, A v) { s[e] = RowType<S>::down(v); }
+    __device__ __forceinline__ void zero() { memset(&raw, 0, BYTES); }
+    __device__ __forceinline__ void up(A (&x)[U]) const
+    {
+        if constexpr (BYTES == 16)
+            unpack16(raw, x, S());
+        else {
+            S s[U];
+            memcpy(s, &raw, BYTES);
+#pragma unroll
+            for (int e = 0; e < U; ++e)
+                x[e] = RowType<S>::up(s[e]);
+        }
+    }
+    __device__ __forceinline__ void set(const A (&x)[U])
+    {
+        if constexpr (BYTES == 16)
+            raw = pack16(x, S());
+        else {
+            S s[U];
+#pragma unroll
+            for (int e = 0; e < U; ++e)
+                s[e] = RowType<S>::down(x[e]);
+            memcpy(&raw, s, BYTES);
+        }
+    }
 };
 
 template <typename S>
@@ -358,8 +369,27 @@ __device__ __forceinline__ void fill_blanks(const RouteArgs<S> &g, int f)
             clear(r);
 }
 
-// R^T x, and with dweight x . ys on the pattern.  KU choices and NV units at a time.
-template <typename S, int U, int KU, int NV>
+// The slots and weights of choices j0 .. j0 + KU of a token; -1 where there is none.
+template <typename S, int KU>
+struct Choices {
+    using A = typename RowType<S>::A;
+    int p[KU];
+    A w[KU];
+    __device__ __forceinline__ void load(const RouteArgs<S> &g, int64_t t, int j0, bool live)
+    {
+#pragma unroll
+        for (int j = 0; j < KU; ++j) {
+            const bool has = live && j0 + j < g.top_k;
+            p[j] = has ? g.slot[t * g.top_k + j0 + j] : -1;
+            if (p[j] >= g.n_slots)
+                p[j] = -1;
+            w[j] = has && g.weight ? g.weight[t * g.top_k + j0 + j] : A(1);
+        }
+    }
+};
+
+// R^T x, and with DW x . ys on the pattern.  KU choices and NV units at a time.
+template <typename S, int U, int KU, int NV, bool DW>
 __global__ void __launch_bounds__(PT) k_route_to_slots(const __grid_constant__ RouteArgs<S> g, int G)
 {
     using A = typename RowType<S>::A;
@@ -374,19 +404,14 @@ __global__ void __launch_bounds__(PT) k_route_to_slots(const __grid_constant__ R
     const int nunits = live ? (int)((g.n_chan + U - 1) / U) : 0;
     const S *x = g.tok + (live ? t : 0) * g.ldtok;
     for (int j0 = 0; j0 < g.top_k; j0 += KU) {
-        int64_t p[KU];
-        A w[KU], dot[KU];
+        Choices<S, KU> ch;
+        ch.load(g, t, j0, live);
+        A dot[KU];
 #pragma unroll
-        for (int j = 0; j < KU; ++j) {
-            const bool has = live && j0 + j < g.top_k;
-            p[j] = has ? g.slot[t * g.top_k + j0 + j] : -1;
-            if (p[j] >= g.n_slots)
-                p[j] = -1;
-            w[j] = has && g.weight ? g.weight[t * g.top_k + j0 + j] : A(1);
+        for (int j = 0; j < KU; ++j)
             dot[j] = A(0);
-        }
         for (int u0 = lane; u0 < nunits; u0 += G * NV) {
-            Unit<S, U> v[NV];
+            Unit<S, U> v[NV], o[DW ? KU : 1][NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int64_t c = (int64_t)(u0 + i * G) * U;
@@ -394,46 +419,53 @@ __global__ void __launch_bounds__(PT) k_route_to_slots(const __grid_constant__ R
                     v[i].load(x + c, (int)min((int64_t)U, g.n_chan - c));
                 else
                     v[i].zero();
-            }
-            if (g.dweight) {
+                if constexpr (DW) {
 #pragma unroll
-                for (int j = 0; j < KU; ++j) {
-                    if (p[j] < 0)
-                        continue;
-                    const S *y = g.slt + p[j] * g.ldslt;
-#pragma unroll
-                    for (int i = 0; i < NV; ++i) {
-                        const int64_t c = (int64_t)(u0 + i * G) * U;
-                        if (u0 + i * G >= nunits)
-                            continue;
-                        Unit<S, U> o;
-                        o.load(y + c, (int)min((int64_t)U, g.n_chan - c));
-#pragma unroll
-                        for (int e = 0; e < U; ++e)
-                            dot[j] = fma_of(v[i].up(e), o.up(e), dot[j]);
+                    for (int j = 0; j < KU; ++j) {
+                        if (ch.p[j] >= 0 && u0 + i * G < nunits)
+                            o[j][i].load(g.slt + ch.p[j] * g.ldslt + c, (int)min((int64_t)U, g.n_chan - c));
+                        else
+                            o[j][i].zero();
                     }
                 }
             }
 #pragma unroll
-            for (int j = 0; j < KU; ++j) {
-                if (p[j] < 0)
+            for (int i = 0; i < NV; ++i) {
+                const int64_t c = (int64_t)(u0 + i * G) * U;
+                if (u0 + i * G >= nunits)
                     continue;
-                S *to = g.slt_out + p[j] * g.ldslt_out;
+                const int left = (int)min((int64_t)U, g.n_chan - c);
+                A f[U];
+                if (DW || g.weight)
+                    v[i].up(f);
+                if constexpr (DW) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int64_t c = (int64_t)(u0 + i * G) * U;
-                    if (u0 + i * G >= nunits)
+                    for (int j = 0; j < KU; ++j) {
+                        A y[U];
+                        o[j][i].up(y);
+                        if (ch.p[j] >= 0)
+#pragma unroll
+                            for (int e = 0; e < U; ++e)
+                                dot[j] = fma_of(f[e], y[e], dot[j]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < KU; ++j) {
+                    if (ch.p[j] < 0)
                         continue;
-                    Unit<S, U> o = v[i];
-                    if (g.weight)
+                    Unit<S, U> r = v[i];
+                    if (g.weight) {
+                        A y[U];
 #pragma unroll
                         for (int e = 0; e < U; ++e)
-                            o.set(e, w[j] * v[i].up(e));
-                    o.store(to + c, (int)min((int64_t)U, g.n_chan - c));
+                            y[e] = ch.w[j] * f[e];
+                        r.set(y);
+                    }
+                    r.store(g.slt_out + ch.p[j] * g.ldslt_out + c, left);
                 }
             }
         }
-        if (g.dweight) {
+        if constexpr (DW) {
             group_sum<A, KU>(dot, G, s_red);
             if (lane == 0 && live)
 #pragma unroll
@@ -444,8 +476,8 @@ __global__ void __launch_bounds__(PT) k_route_to_slots(const __grid_constant__ R
     }
 }
 
-// R ys, and with dweight x . ys on the pattern.
-template <typename S, int U, int KU, int NV>
+// R ys, and with DW x . ys on the pattern: in the same pass with up to KU choices, after the sums with more.
+template <typename S, int U, int KU, int NV, bool DW>
 __global__ void __launch_bounds__(PT) k_route_to_tokens(const __grid_constant__ RouteArgs<S> g, int G)
 {
     using A = typename RowType<S>::A;
@@ -454,24 +486,14 @@ __global__ void __launch_bounds__(PT) k_route_to_tokens(const __grid_constant__ 
     const int lane = threadIdx.x & (G - 1);
     const bool live = t < g.n_tokens;
     const int nunits = live ? (int)((g.n_chan + U - 1) / U) : 0;
-    const bool one = g.top_k <= KU;            // all choices at once: the dot products pass with the sum
-    int64_t p[KU];
-    A w[KU], dot[KU];
-    auto choices = [&](int j0) {
-#pragma unroll
-        for (int j = 0; j < KU; ++j) {
-            const bool has = live && j0 + j < g.top_k;
-            p[j] = has ? g.slot[t * g.top_k + j0 + j] : -1;
-            if (p[j] >= g.n_slots)
-                p[j] = -1;
-            w[j] = has && g.weight ? g.weight[t * g.top_k + j0 + j] : A(1);
-        }
-    };
-    const S *x = g.dweight ? g.tok + (live ? t : 0) * g.ldtok : nullptr;
-    choices(0);
+    const bool one = g.top_k <= KU;
+    Choices<S, KU> ch;
+    ch.load(g, t, 0, live);
+    A dot[KU];
 #pragma unroll
     for (int j = 0; j < KU; ++j)
         dot[j] = A(0);
+    const S *x = DW ? g.tok + (live ? t : 0) * g.ldtok : nullptr;
     for (int u0 = lane; u0 < nunits; u0 += G * NV) {
         A acc[NV][U];
 #pragma unroll
@@ -481,83 +503,88 @@ __global__ void __launch_bounds__(PT) k_route_to_tokens(const __grid_constant__ 
                 acc[i][e] = A(0);
         for (int j0 = 0; j0 < g.top_k; j0 += KU) {
             if (!one)
-                choices(j0);
-            Unit<S, U> o[KU][NV];
+                ch.load(g, t, j0, live);
+            Unit<S, U> o[KU][NV], v[DW ? NV : 1];
 #pragma unroll
-            for (int j = 0; j < KU; ++j)
+            for (int i = 0; i < NV; ++i) {
+                const int64_t c = (int64_t)(u0 + i * G) * U;
+                const bool in = u0 + i * G < nunits;
+                const int left = (int)min((int64_t)U, g.n_chan - c);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int64_t c = (int64_t)(u0 + i * G) * U;
-                    if (p[j] >= 0 && u0 + i * G < nunits)
-                        o[j][i].load(g.slt + p[j] * g.ldslt + c, (int)min((int64_t)U, g.n_chan - c));
+                for (int j = 0; j < KU; ++j) {
+                    if (ch.p[j] >= 0 && in)
+                        o[j][i].load(g.slt + ch.p[j] * g.ldslt + c, left);
                     else
                         o[j][i].zero();
                 }
-            if (one && x) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int64_t c = (int64_t)(u0 + i * G) * U;
-                    if (u0 + i * G >= nunits)
-                        continue;
-                    Unit<S, U> v;
-                    v.load(x + c, (int)min((int64_t)U, g.n_chan - c));
-#pragma unroll
-                    for (int j = 0; j < KU; ++j)
-                        if (p[j] >= 0)
-#pragma unroll
-                            for (int e = 0; e < U; ++e)
-                                dot[j] = fma_of(v.up(e), o[j][i].up(e), dot[j]);
+                if constexpr (DW) {
+                    v[i].zero();
+                    if (one && in)
+                        v[i].load(x + c, left);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < KU; ++j)
-                if (p[j] >= 0)
+            for (int i = 0; i < NV; ++i) {
+                A f[U];
+                if constexpr (DW)
+                    v[i].up(f);
 #pragma unroll
-                    for (int i = 0; i < NV; ++i)
+                for (int j = 0; j < KU; ++j) {
+                    if (ch.p[j] < 0)
+                        continue;
+                    A y[U];
+                    o[j][i].up(y);
 #pragma unroll
-                        for (int e = 0; e < U; ++e)
-                            acc[i][e] = fma_of(w[j], o[j][i].up(e), acc[i][e]);
+                    for (int e = 0; e < U; ++e) {
+                        if constexpr (DW)
+                            dot[j] = fma_of(f[e], y[e], dot[j]);
+                        acc[i][e] = fma_of(ch.w[j], y[e], acc[i][e]);
+                    }
+                }
+            }
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int64_t c = (int64_t)(u0 + i * G) * U;
             if (u0 + i * G >= nunits)
                 continue;
-            Unit<S, U> o;
-#pragma unroll
-            for (int e = 0; e < U; ++e)
-                o.set(e, acc[i][e]);
-            o.store(g.tok_out + t * g.ldtok_out + c, (int)min((int64_t)U, g.n_chan - c));
+            Unit<S, U> r;
+            r.set(acc[i]);
+            r.store(g.tok_out + t * g.ldtok_out + c, (int)min((int64_t)U, g.n_chan - c));
         }
     }
-    if (!g.dweight)
-        return;
-    for (int j0 = 0; j0 < g.top_k; j0 += KU) {
-        if (!one) {
-            choices(j0);
-#pragma unroll
-            for (int j = 0; j < KU; ++j)
-                dot[j] = A(0);
-            for (int u = lane; u < nunits; u += G) {
-                const int64_t c = (int64_t)u * U;
-                Unit<S, U> v, o;
-                v.load(x + c, (int)min((int64_t)U, g.n_chan - c));
+    if constexpr (DW) {
+        for (int j0 = 0; j0 < g.top_k; j0 += KU) {
+            if (!one) {
+                ch.load(g, t, j0, live);
 #pragma unroll
                 for (int j = 0; j < KU; ++j)
-                    if (p[j] >= 0) {
-                        o.load(g.slt + p[j] * g.ldslt + c, (int)min((int64_t)U, g.n_chan - c));
+                    dot[j] = A(0);
+                for (int u = lane; u < nunits; u += G) {
+                    const int64_t c = (int64_t)u * U;
+                    const int left = (int)min((int64_t)U, g.n_chan - c);
+                    Unit<S, U> v;
+                    v.load(x + c, left);
+                    A f[U], y[U];
+                    v.up(f);
 #pragma unroll
-                        for (int e = 0; e < U; ++e)
-                            dot[j] = fma_of(v.up(e), o.up(e), dot[j]);
-                    }
+                    for (int j = 0; j < KU; ++j)
+                        if (ch.p[j] >= 0) {
+                            v.load(g.slt + ch.p[j] * g.ldslt + c, left);
+                            v.up(y);
+#pragma unroll
+                            for (int e = 0; e < U; ++e)
+                                dot[j] = fma_of(f[e], y[e], dot[j]);
+                        }
+                }
             }
-        }
-        group_sum<A, KU>(dot, G, s_red);
-        if (lane == 0 && live)
+            group_sum<A, KU>(dot, G, s_red);
+            if (lane == 0 && live)
 #pragma unroll
-            for (int j = 0; j < KU; ++j)
-                if (j0 + j < g.top_k)
-                    g.dweight[t * g.top_k + j0 + j] = dot[j];
+                for (int j = 0; j < KU; ++j)
+                    if (j0 + j < g.top_k)
+                        g.dweight[t * g.top_k + j0 + j] = dot[j];
+        }
     }
 }
 
@@ -571,7 +598,7 @@ static inline int group_of(int64_t n_chan, int U, int NV)
     return G;
 }
 
-template <typename S, int U, int KU, int NV>
+template <typename S, int U, int KU, int NV, bool DW>
 sla_status launch_product(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
 {
     const int G = group_of(g.n_chan, U, NV);
@@ -580,22 +607,29 @@ sla_status launch_product(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
         // a fill block for every 64 KiB of slot rows that may be blank, at most two an SM
         const int64_t bytes = g.n_slots * g.n_chan * (int64_t)sizeof(S);
         g.fill_blocks = (int)std::max<int64_t>(1, std::min<int64_t>(296, bytes >> 16));
-        k_route_to_slots<S, U, KU, NV><<<(unsigned)(blocks + g.fill_blocks), PT, 0, s>>>(g, G);
+        k_route_to_slots<S, U, KU, NV, DW><<<(unsigned)(blocks + g.fill_blocks), PT, 0, s>>>(g, G);
     } else if (blocks > 0)
-        k_route_to_tokens<S, U, KU, NV><<<(unsigned)blocks, PT, 0, s>>>(g, G);
+        k_route_to_tokens<S, U, KU, NV, DW><<<(unsigned)blocks, PT, 0, s>>>(g, G);
     SLA_CUDA_TRY(cudaGetLastError());
     return SLA_SUCCESS;
 }
 
-// About 8 loads in flight a thread: KU choices times NV units (fp64 and short units alike).
+template <typename S, int U, int KU, int NV>
+sla_status launch_dw(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
+{
+    return g.dweight ? launch_product<S, U, KU, NV, true>(g, to_slots, s)
+                     : launch_product<S, U, KU, NV, false>(g, to_slots, s);
+}
+
+// KU choices times NV units in flight a thread, about 8 rows' units.
 template <typename S, int U>
 sla_status launch_unit(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
 {
     if (g.top_k <= 2)
-        return launch_product<S, U, 2, 4>(g, to_slots, s);
+        return launch_dw<S, U, 2, 2>(g, to_slots, s);
     if (g.top_k <= 4)
-        return launch_product<S, U, 4, 2>(g, to_slots, s);
-    return launch_product<S, U, 8, 1>(g, to_slots, s);
+        return launch_dw<S, U, 4, 2>(g, to_slots, s);
+    return launch_dw<S, U, 8, 1>(g, to_slots, s);
 }
 
 template <typename S>
