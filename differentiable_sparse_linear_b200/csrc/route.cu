@@ -306,32 +306,43 @@ struct RouteArgs {
     A *dweight;
 };
 
-// Sums of K values over a group of G threads (a power of two, a warp at least), in a fixed order; valid in its
-// first thread.
+// Sums of K values (a power of two) over a group of G threads (a power of two, a warp at least), in a fixed
+// order; the j-th ends in the group's j-th thread.  Within a warp the lanes first share the values out, each exchange
+// halving the number a lane carries (K - 1 + 5 - log2 K exchanges instead of 5 K).
 template <typename A, int K>
-__device__ __forceinline__ void group_sum(A (&d)[K], int G, A (*s_red)[K])
+__device__ __forceinline__ A group_sums(A (&d)[K], int G, A (*s_red)[K])
 {
+    const int lane = threadIdx.x & 31;
+    int bit = 1;
 #pragma unroll
-    for (int j = 0; j < K; ++j)
-        for (int o = 16; o > 0; o >>= 1)
-            d[j] += __shfl_xor_sync(0xffffffffu, d[j], o);
-    if (G > 32) {
-        const int warp = threadIdx.x >> 5;
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0)
+    for (int n = K / 2; n > 0; n /= 2, bit *= 2) {
+        const bool upper = lane & bit;
 #pragma unroll
-            for (int j = 0; j < K; ++j)
-                s_red[warp][j] = d[j];
-        __syncthreads();
-        if ((threadIdx.x & (G - 1)) == 0)
-#pragma unroll
-            for (int j = 0; j < K; ++j) {
-                A t = A(0);
-                for (int w = 0; w < G / 32; ++w)
-                    t += s_red[warp + w][j];
-                d[j] = t;
-            }
+        for (int j = 0; j < n; ++j) {
+            const A send = upper ? d[j] : d[j + n], keep = upper ? d[j + n] : d[j];
+            d[j] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+        }
     }
+    for (; bit < 32; bit *= 2)
+        d[0] += __shfl_xor_sync(0xffffffffu, d[0], bit);
+    // the lane whose low bits, read from the lowest up, spell j from its highest bit down has value j
+    int at = 0;
+#pragma unroll
+    for (int n = K / 2, b = 1; n > 0; n /= 2, b *= 2)
+        at |= (lane & n) ? b : 0;
+    if (G == 32)
+        return __shfl_sync(0xffffffffu, d[0], at);
+    const int warp = threadIdx.x >> 5, first = (threadIdx.x & ~(G - 1)) >> 5, j = threadIdx.x & (G - 1);
+    const A mine = __shfl_sync(0xffffffffu, d[0], at);
+    __syncthreads();
+    if (lane < K)
+        s_red[warp][lane] = mine;
+    __syncthreads();
+    A t = A(0);
+    if (j < K)
+        for (int w = 0; w < G / 32; ++w)
+            t += s_red[first + w][j];
+    return t;
 }
 
 // Zeros in the slots without an entry, a row a warp: block f of the fill blocks takes the padding rows r of
@@ -466,12 +477,9 @@ __global__ void __launch_bounds__(PT) k_route_to_slots(const __grid_constant__ R
             }
         }
         if constexpr (DW) {
-            group_sum<A, KU>(dot, G, s_red);
-            if (lane == 0 && live)
-#pragma unroll
-                for (int j = 0; j < KU; ++j)
-                    if (j0 + j < g.top_k)
-                        g.dweight[t * g.top_k + j0 + j] = dot[j];
+            const A sum = group_sums<A, KU>(dot, G, s_red);
+            if (live && lane < KU && j0 + lane < g.top_k)
+                g.dweight[t * g.top_k + j0 + lane] = sum;
         }
     }
 }
@@ -578,30 +586,32 @@ __global__ void __launch_bounds__(PT) k_route_to_tokens(const __grid_constant__ 
                         }
                 }
             }
-            group_sum<A, KU>(dot, G, s_red);
-            if (lane == 0 && live)
-#pragma unroll
-                for (int j = 0; j < KU; ++j)
-                    if (j0 + j < g.top_k)
-                        g.dweight[t * g.top_k + j0 + j] = dot[j];
+            const A sum = group_sums<A, KU>(dot, G, s_red);
+            if (live && lane < KU && j0 + lane < g.top_k)
+                g.dweight[t * g.top_k + j0 + lane] = sum;
         }
     }
 }
 
-// Threads a token: its units shared out NV each, a warp at least, a block at most.
-static inline int group_of(int64_t n_chan, int U, int NV)
+// Threads a token, a warp at least and a block at most: its units NV at a time, in up to four turns where there
+// are tokens enough to fill the GPU's threads all the same (fewer threads a token spend less on its plan and
+// on the sums over the group).
+static inline int group_of(int64_t n_tokens, int64_t n_chan, int U, int NV)
 {
-    const int64_t want = (n_chan + (int64_t)U * NV - 1) / ((int64_t)U * NV);
-    int G = 32;
-    while (G < PT && G < want)
-        G *= 2;
-    return G;
+    const int64_t nunits = (n_chan + U - 1) / U;
+    for (int turns = 4;; turns /= 2) {
+        int G = 32;
+        while (G < PT && (int64_t)G * NV * turns < nunits)
+            G *= 2;
+        if (turns == 1 || n_tokens * G >= 148 * 2048)
+            return G;
+    }
 }
 
 template <typename S, int U, int KU, int NV, bool DW>
 sla_status launch_product(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
 {
-    const int G = group_of(g.n_chan, U, NV);
+    const int G = group_of(g.n_tokens, g.n_chan, U, NV);
     const int64_t blocks = (g.n_tokens + PT / G - 1) / (PT / G);
     if (to_slots) {
         // a fill block for every 64 KiB of slot rows that may be blank, at most two an SM
@@ -621,15 +631,16 @@ sla_status launch_dw(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
                      : launch_product<S, U, KU, NV, false>(g, to_slots, s);
 }
 
-// KU choices times NV units in flight a thread, about 8 rows' units.
+// KU choices times NV units in flight a thread, more units where they are short.
 template <typename S, int U>
 sla_status launch_unit(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
 {
+    constexpr int M = U * sizeof(S) == 16 ? 1 : 2;
     if (g.top_k <= 2)
-        return launch_dw<S, U, 2, 2>(g, to_slots, s);
+        return launch_dw<S, U, 2, 2 * M>(g, to_slots, s);
     if (g.top_k <= 4)
-        return launch_dw<S, U, 4, 2>(g, to_slots, s);
-    return launch_dw<S, U, 8, 1>(g, to_slots, s);
+        return launch_dw<S, U, 4, 2 * M>(g, to_slots, s);
+    return launch_dw<S, U, 8, M>(g, to_slots, s);
 }
 
 template <typename S>
