@@ -25,9 +25,9 @@ __global__ void __launch_bounds__(RT)
                 h[r * ldh + c] = S(0.0f);
             continue;
         }
-        A ca, w;
-        gate_of<GATE, sizeof(S) == 2>(R::up(a[r * lda + c]), ca, w);
-        const A v = fma_of(ca, state[i * lds + c], w * R::up(b[r * ldb + c]));
+        A z[2] = {R::up(a[r * lda + c]), A(0)}, ca[2], w[2];
+        gates_of<GATE, sizeof(S) == 2>(z, ca, w);
+        const A v = fma_of(ca[0], state[i * lds + c], mul_of(w[0], R::up(b[r * ldb + c])));
         state[i * lds + c] = v;
         h[r * ldh + c] = R::down(v);
     }
@@ -83,6 +83,21 @@ dim3 grid_of(int64_t n_chan, int64_t rows)
 }
 
 }  // namespace
+
+EncodeTiled encode_tiled()
+{
+    static const EncodeTiled found = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult got;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &got);
+        if (e != cudaSuccess || got != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return (EncodeTiled)p;
+    }();
+    return found;
+}
 
 int sm_count()
 {

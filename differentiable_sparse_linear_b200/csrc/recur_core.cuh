@@ -11,16 +11,21 @@
 // 8 threads make a row, so the tile has NR = 4 NW runs.  Tiles are taken by ticket, chunk-major, by
 // one persistent block per SM.
 //
-// One block runs four kinds of work at the same time, tile i being the oldest:
-//   loads       each thread copies its own rows of tile i + NS into its own place in shared memory
-//               (cp.async), so staging needs no barrier;
-//   pass 1      tile i + 1: each thread's (A, H), left in shared memory;
-//   scan warps  tile i + 1, four threads a channel, each over a quarter of the runs in order: the tile's (A, H),
-//               published for later chunks; the state that enters it, from the published results of
-//               earlier chunks; the state that enters every run;
-//   pass 2      tile i: every row from the state that enters it, in the order of the formula, and the stores.
-// A plan warp takes the tickets and finds the sequence borders inside a tile, NS tiles ahead.  So each
-// input is read once and the wait on earlier chunks passes while other tiles are worked on.
+// One block runs these at the same time, tile i being the oldest:
+//   pass 1      tile i + 1: the coefficients, kept in registers for pass 2, and each thread's (A, H), left in
+//               shared memory;
+//   map warps   tile i + 1, one thread a channel, over the runs in order: the tile's (A, H), published for later
+//               chunks, and for every run the map of the runs in front of it;
+//   state warps tile i + 1: the state that enters it, from what earlier chunks published; its own leaving
+//               state, published;
+//   pass 2      tile i: the state that enters the run, every row from it in the order of the formula, and the
+//               stores;
+//   plan warp   the ticket of tile i + 3, the sequence borders in it, and its rows into shared memory by one tensor
+//               copy an input (backward, what only pass 2 reads: of tile i + 1).  Where rows are not aligned to
+//               16 bytes every compute thread copies its own values instead, by units of 4 bytes or one
+//               by one.
+// So each input is read once and each gate evaluated once, and the wait on earlier chunks passes while the
+// compute warps are at another tile.  They meet once a tile, where they take over the entering states.
 //
 // Across chunks a channel publishes (A, H) as soon as pass 1 has them, and the state that leaves the
 // chunk, x', once it knows the state that enters.  A later chunk goes back to the nearest chunk whose x' is
@@ -37,6 +42,7 @@
 // of zeros.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -75,6 +81,7 @@ struct RecurArgs {
     const A *enter;            // forward h0, backward dh_last
     const A *before;           // backward: h0
     A *leave;                  // forward h_last, backward dh0
+    CUtensorMap map[4];        // of the inputs, where rows go by tensor copies
     int fill;                  // zeros in rows outside every sequence
     unsigned *ticket;          // NULL with one chunk
     unsigned long long *agg;   // [n_chunks][n_chan] words (fp64: two each)
@@ -86,35 +93,21 @@ struct RecurShape {
     static constexpr int NIN = REV ? (GATE == SLA_GATE_SIGMOID ? 4 : 3) : 2;
     static constexpr int V = 16 / (int)sizeof(S);          // channels of a thread
     static constexpr int W = 8 * V;                        // channels of a tile
-    static constexpr int R = 4;
-    // Warps and stages by shared memory (three stages, so that a load has a tile's time to arrive)
-    static constexpr int NW = !REV ? 12 : NIN == 3 ? 10 : 7;
-    static constexpr int NS = 3;
-    static constexpr int NP = NS + 1;                      // plan slots
+    static constexpr int R = 4;                            // rows of a run
+    static constexpr int N1 = 2;                           // inputs that pass 1 reads; the others wait for pass 2
+    // Compute warps: 16 warps of 128 registers in all, or what shared memory allows
+    static constexpr int NW = !REV ? 11 : NIN == 3 ? 10 : 9;
+    static constexpr int NS = 3;                           // tiles that plan and loads are ahead
+    static constexpr int NZ = 2;                           // stages of input 0, done with after pass 1
+    static constexpr int N1S = 4;                          // stages of input 1
+    static constexpr int NX = 2;                           // stages of the inputs that only pass 2 reads
+    static constexpr int NB = 2;                           // tiles between pass 1 and pass 2
+    static constexpr int NP = NS + 2;                      // plan slots
     static constexpr int NR = NW * 4;                      // runs
     static constexpr int C = NR * R;
     static constexpr int NC = NW * 32;                     // compute threads
-    static constexpr int RQ = NR / 4;                      // runs of a quarter of the tile
-    static constexpr int NSCAN = W * 4;                    // scan threads: four a channel, a quarter each
-    static constexpr int NT = NC + NSCAN + 32;
-};
-
-struct TilePlan {
-    int tile;                  // -1: no more tiles
-    int chunk, cb;
-    int lo, hi;                // positions of the tile inside [first, last) row of all sequences
-    int seg;                   // borders or rows outside the sequences in the tile: use the flags
-};
-
-template <typename S, int GATE, bool REV>
-struct RecurSmem {
-    using P = RecurShape<S, GATE, REV>;
-    using A = typename RowType<S>::A;
-    uint4 stage[P::NS][P::NIN][P::R][P::NC];
-    // per run and channel (A, H); the scan leaves the state that enters the run in H's place
-    A mapA[2][P::NR][P::W], mapH[2][P::NR][P::W];
-    int begin[P::NP][P::C], finish[P::NP][P::C];   // sequence the scan enters / leaves at a position, or -1
-    TilePlan plan[P::NP];
+    static constexpr int NK = (W + 31) / 32 * 32;          // map threads, and state threads
+    static constexpr int NT = NC + 2 * NK + 32;
 };
 
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
@@ -131,6 +124,45 @@ __device__ __forceinline__ void copy_async(void *dst, const void *src, int bytes
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(d), "l"(src), "r"(bytes), "n"(B) : "memory");
+}
+
+// Barriers in shared memory that copies arrive at.
+__device__ __forceinline__ unsigned smem_at(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(unsigned long long *bar, int count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_at(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(unsigned long long *bar, int bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_at(bar)), "r"(bytes) : "memory");
+}
+// A box of a tile's rows, from column x (a multiple of 16 bytes) and row y (which may lie in front of the first)
+__device__ __forceinline__ void box_in(void *dst, const CUtensorMap *map, int x, int y, unsigned long long *bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                     smem_at(dst)),
+                 "l"(map), "r"(x), "r"(y), "r"(smem_at(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_after_copies(unsigned long long *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_at(bar)) : "memory");
+}
+// Waits for the phase to end, a bounded number of times; false if it did not.
+__device__ __forceinline__ bool mbar_wait(unsigned long long *bar, unsigned parity)
+{
+    for (int i = 0; i < 1 << 22; ++i) {
+        unsigned done;
+        asm volatile("{ .reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p; }"
+                     : "=r"(done)
+                     : "r"(smem_at(bar)), "r"(parity)
+                     : "memory");
+        if (done)
+            return true;
+    }
+    return false;
 }
 
 // ------------------------------------------------------------------ affine maps
@@ -179,7 +211,7 @@ __device__ __forceinline__ void st_word(unsigned *p, unsigned v)
     asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// fp32 arithmetic: A's upper 32 bits as fp64 (its range; 2^-21 relative, once per chunk) and H in one word.
+// fp32 arithmetic: one word of A's upper 32 bits as fp64 (its range; 2^-21 relative, once per chunk) and H.
 // fp64: a word each.
 template <typename A>
 struct Words;
@@ -187,22 +219,40 @@ template <>
 struct Words<float> {
     static constexpr int N = 1;
     using Inc = unsigned;
+    using Map = unsigned;
+    static constexpr unsigned CONST = 0x80000000u;         // packed A of a constant map
+    static __device__ __forceinline__ bool fixed(unsigned a) { return a == CONST; }
     unsigned long long w[1];
-    // A as it is published: every user of the map, its own chunk included, applies this one
-    static __device__ __forceinline__ double round_a(double a)
+    // A as it is published: every user of the map, its own chunk included, applies this one.  An A within fp32's
+    // range is converted by shifts (subnormal ones are 0), an overflowed one is `wide`.
+    static __device__ __forceinline__ unsigned pack(float a)
+    {
+        const unsigned b = __float_as_uint(a), mag = b & 0x7fffffffu;
+        return (b & 0x80000000u) | (mag < 0x00800000u ? 0u : ((mag + 4u) >> 3) + (896u << 20));
+    }
+    static __device__ __forceinline__ unsigned pack(double a)
     {
         if (!(a == a))
-            return __hiloint2double(0x7ff80000, 0);
-        return __longlong_as_double((__double_as_longlong(a) + 0x80000000ll) & ~0xffffffffll);
+            return 0x7ff80000u;
+        return (unsigned)(((unsigned long long)__double_as_longlong(a) + 0x80000000ull) >> 32);
     }
-    static __device__ __forceinline__ void put(unsigned long long *p, double a, float h)
+    static __device__ __forceinline__ float apply(unsigned a, float x, float h)
     {
-        st_word(p, ((unsigned long long)(unsigned)__double2hiint(a) << 32) | __float_as_uint(h));
+        const unsigned mag = a & 0x7fffffffu;
+        if (mag >= ((1023u + 127u) << 20))                 // beyond fp32, and NaN
+            return apply_wide(__hiloint2double((int)a, 0), x, h);
+        const unsigned f = mag < (897u << 20) ? 0u : (mag - (896u << 20)) << 3;
+        return __fmaf_rn(__uint_as_float((a & 0x80000000u) | f), x, h);
+    }
+    // within fp32's range
+    static __device__ __forceinline__ bool finite(unsigned a) { return (a & 0x7fffffffu) < ((1023u + 128u) << 20); }
+    static __device__ __forceinline__ void put(unsigned long long *p, unsigned a, float h)
+    {
+        st_word(p, ((unsigned long long)a << 32) | __float_as_uint(h));
     }
     __device__ __forceinline__ void load(const unsigned long long *p) { w[0] = ld_word(p); }
     __device__ __forceinline__ bool there() const { return (unsigned)(w[0] >> 32) != 0xffffffffu; }
-    __device__ __forceinline__ double a() const { return __hiloint2double((int)(w[0] >> 32), 0); }
-    __device__ __forceinline__ float h() const { return __uint_as_float((unsigned)w[0]); }
+    __device__ __forceinline__ float of(float x) const { return apply((unsigned)(w[0] >> 32), x, __uint_as_float((unsigned)w[0])); }
     static __device__ __forceinline__ unsigned inc_bits(float x) { return x == x ? __float_as_uint(x) : 0x7fffffffu; }
     static __device__ __forceinline__ float inc_value(unsigned v) { return __uint_as_float(v); }
     static __device__ __forceinline__ bool inc_there(unsigned v) { return v != 0xffffffffu; }
@@ -211,13 +261,17 @@ template <>
 struct Words<double> {
     static constexpr int N = 2;
     using Inc = unsigned long long;
+    using Map = double;
+    static __device__ __forceinline__ bool fixed(double a) { return is_const(a); }
     static constexpr unsigned long long NONE = ~0ull, QUIET = 0x7ff8000000000000ull;
     unsigned long long w[2];
-    static __device__ __forceinline__ double round_a(double a) { return a; }
     static __device__ __forceinline__ unsigned long long bits(double x)
     {
         return x == x ? (unsigned long long)__double_as_longlong(x) : QUIET;
     }
+    static __device__ __forceinline__ double pack(double a) { return a; }
+    static __device__ __forceinline__ bool finite(double a) { return isfinite(a); }
+    static __device__ __forceinline__ double apply(double a, double x, double h) { return apply_wide(a, x, h); }
     static __device__ __forceinline__ void put(unsigned long long *p, double a, double h)
     {
         st_word(p, bits(a));
@@ -229,105 +283,130 @@ struct Words<double> {
         w[1] = ld_word(p + 1);
     }
     __device__ __forceinline__ bool there() const { return w[0] != NONE && w[1] != NONE; }
-    __device__ __forceinline__ double a() const { return __longlong_as_double((long long)w[0]); }
-    __device__ __forceinline__ double h() const { return __longlong_as_double((long long)w[1]); }
+    __device__ __forceinline__ double of(double x) const
+    {
+        return apply(__longlong_as_double((long long)w[0]), x, __longlong_as_double((long long)w[1]));
+    }
     static __device__ __forceinline__ unsigned long long inc_bits(double x) { return bits(x); }
     static __device__ __forceinline__ double inc_value(unsigned long long v) { return __longlong_as_double((long long)v); }
     static __device__ __forceinline__ bool inc_there(unsigned long long v) { return v != NONE; }
 };
 
-// The state that enters `chunk` at one channel, by the four lanes l, l + 8, l + 16, l + 24 of a warp: back to the
-// nearest chunk whose leaving state is there (4 K chunks a round trip, K a lane), then forward over the
-// maps behind it, one after the other.  All lanes of the warp call it; `want` is false where no state is needed.
-template <typename A>
-__device__ __forceinline__ A state_before(int chunk, int64_t n_chan, int64_t ch, bool want, int lane,
-                                          const unsigned long long *agg, const typename Words<A>::Inc *inc)
-{
+// One channel's words of the N chunks before `chunk`, nearest first.
+template <typename A, int K>
+struct Window {
     using Wd = Words<A>;
-    constexpr int K = 4, OPEN = 1 << 20;
-    const unsigned all = 0xffffffffu;
-    const int q = lane >> 3, l8 = lane & 7;
-    bool done = !want, gave_up = false;
-    A x = A(0);
-    int last = chunk - 1, from = chunk;
-    for (int polls = 0;; ++polls) {
-        typename Wd::Inc v[K];
-        Wd m[K];
-        int mine = OPEN;               // 2 * (distance) of the nearest leaving state, + 1 if a map is missing first
-        if (!done) {
+    typename Wd::Inc v[K];
+    Wd m[K];
+    __device__ __forceinline__ void load(int last, int64_t n_chan, int64_t ch, const unsigned long long *agg,
+                                         const typename Wd::Inc *inc)
+    {
+        const int64_t at = (int64_t)last * n_chan + ch;
+        const typename Wd::Inc *pi = inc + at;
+        const unsigned long long *pm = agg + at * Wd::N;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const int64_t at = (int64_t)max(last - q * K - k, 0) * n_chan + ch;
-                v[k] = ld_word(inc + at);
-                m[k].load(agg + at * Wd::N);
+        for (int k = 0; k < K; ++k) {
+            v[k] = ld_word(pi);
+            m[k].load(pm);
+            if (last - k > 0) {
+                pi -= n_chan;
+                pm -= n_chan * Wd::N;
             }
-#pragma unroll
-            for (int k = K - 1; k >= 0; --k)
-                if (last - q * K - k >= 0) {
-                    if (Wd::inc_there(v[k]))
-                        mine = 2 * (q * K + k);
-                    else if (!m[k].there())
-                        mine = 2 * (q * K + k) + 1;
-                }
-        }
-        mine = min(mine, __shfl_xor_sync(all, mine, 8));
-        mine = min(mine, __shfl_xor_sync(all, mine, 16));
-        const bool found = !done && mine < OPEN && !(mine & 1);
-        if (__any_sync(all, found)) {
-            const int fq = mine / 2 / K, fk = mine / 2 % K;
-            A y = A(0);
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (found && q == fq && k == fk)
-                    y = Wd::inc_value(v[k]);
-#pragma unroll
-            for (int s = 3; s >= 0; --s) {
-                if (found && q == s && s <= fq) {
-#pragma unroll
-                    for (int k = K - 1; k >= 0; --k)
-                        if (s < fq || k < fk)
-                            y = apply_wide(m[k].a(), y, m[k].h());
-                }
-                const A o = __shfl_sync(all, y, s * 8 + l8);
-                if (q < s && s <= fq)
-                    y = o;
-            }
-            y = __shfl_sync(all, y, l8);
-            if (found) {
-                x = y;
-                from = last + 1;
-                done = true;
-            }
-        }
-        if (!done && mine == OPEN && last - 4 * K >= 0)
-            last -= 4 * K;
-        if (!__any_sync(all, !done))
-            break;
-        if (polls >= 1 << 22) {
-            gave_up = !done;
-            break;
         }
     }
-    // the maps that were passed on the way back
-    while (__any_sync(all, from < chunk)) {
-        Wd m[K];
+    // Chunk `last - k` is the nearest whose leaving state is there: the state behind all of them in x.
+    // 1: yes; 0: a map is missing in front of it; -1: all maps are there and no state
+    __device__ __forceinline__ int look(int last, A &x) const
+    {
+        int found = -1;
+        bool open = true;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            m[k].load(agg + ((int64_t)min(from + q * K + k, chunk - 1) * n_chan + ch) * Wd::N);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if (q == s) {
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (from + q * K + k < chunk)
-                        x = apply_wide(m[k].a(), x, m[k].h());
+            if (open && found < 0) {
+                if (last - k >= 0 && Wd::inc_there(v[k])) {
+                    found = k;
+                    x = Wd::inc_value(v[k]);
+                } else
+                    open = last - k >= 0 && m[k].there();
             }
-            x = __shfl_sync(all, x, s * 8 + l8);
-        }
-        from += 4 * K;
+        if (found < 0)
+            return open ? -1 : 0;
+#pragma unroll
+        for (int k = K - 2; k >= 0; --k)
+            if (k < found)
+                x = m[k].of(x);
+        return 1;
     }
-    return gave_up ? A(NAN) : x;
+};
+
+// The state that enters `chunk` at one channel: back to the nearest chunk whose leaving state is there, then
+// forward over the maps behind it, one after the other.  Four chunks a look, or 16 (fp64: 8) from the start where
+// more than four chunks are at work at a time (`deep`).
+template <typename A>
+__device__ __forceinline__ A state_before(int chunk, int64_t n_chan, int64_t ch, bool deep, const unsigned long long *agg,
+                                          const typename Words<A>::Inc *inc)
+{
+    constexpr int K = 16 / Words<A>::N, LIMIT = 1 << 22;
+    A x = A(0);
+    int polls = 0, got = -1, last = chunk - 1;
+    if (!deep) {
+        Window<A, 4> near;
+        do {
+            near.load(last, n_chan, ch, agg, inc);
+            got = near.look(last, x);
+        } while (got == 0 && ++polls < LIMIT);
+        if (got > 0)
+            return x;
+        last -= 4;
+    }
+    Window<A, K> far;
+    while (got <= 0 && polls < LIMIT && last >= 0) {
+        far.load(last, n_chan, ch, agg, inc);
+        got = far.look(last, x);
+        if (got < 0)
+            last -= K;
+        ++polls;
+    }
+    if (got <= 0)
+        return A(NAN);                                     // gave up
+    for (int from = last + 1; from < chunk; from += K) {
+        Words<A> m[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            m[k].load(agg + ((int64_t)min(from + k, chunk - 1) * n_chan + ch) * Words<A>::N);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (from + k < chunk)
+                x = m[k].of(x);
+    }
+    return x;
 }
+
+struct TilePlan {
+    int tile;                  // -1: no more tiles
+    int chunk, cb;
+    int lo, hi;                // positions of the tile inside [first, last) row of all sequences
+    int seg;                   // borders or rows outside the sequences in the tile: use the flags
+};
+
+template <typename S, int GATE, bool REV>
+struct RecurSmem {
+    using P = RecurShape<S, GATE, REV>;
+    using A = typename RowType<S>::A;
+    static constexpr int NE = P::NIN > P::N1 ? P::NIN - P::N1 : 1;
+    // rows of 128 bytes
+    uint4 stage0[P::NZ][P::C][8];
+    uint4 stage1[P::N1S][P::C][8];
+    uint4 stage2[NE][P::NIN > P::N1 ? P::NX : 1][P::NIN > P::N1 ? P::C : 1][8];
+    unsigned long long full[P::N1S], late[P::NX];
+    // per run and channel (A, H); then the map of the runs in front of it
+    A mapA[P::NB][P::NR][P::W], mapH[P::NB][P::NR][P::W];
+    typename Words<A>::Map tileA[P::NB][P::W];     // the tile's map as published
+    A tileH[P::NB][P::W];
+    A enter[P::NB][P::W];                          // the state that enters the tile
+    int begin[P::NP][P::C], finish[P::NP][P::C];   // sequence the scan enters / leaves at a position, or -1
+    TilePlan plan[P::NP];
+};
 
 // ------------------------------------------------------------------ the kernel
 template <typename S, int GATE, int U, bool REV>
@@ -337,13 +416,14 @@ struct Recur {
     using A = typename RT::A;
     using Sm = RecurSmem<S, GATE, REV>;
     static constexpr int V = P::V, R = P::R, C = P::C, NC = P::NC;
-    static constexpr int UNITS = V / U;                    // a thread's channels: UNITS groups of U contiguous ones
+    static constexpr int UNITS = V / U;                    // copies and stores of 16 bytes go in units of U values
 
     const RecurArgs<S> &g;
     Sm &sm;
     const int tid, warp, lane, l8;
     const int run;                                         // the thread's run of a tile
     const int p0;                                          // its first position
+    bool lost = false;                                     // a load did not arrive
 
     __device__ __forceinline__ Recur(const RecurArgs<S> &g_, Sm &sm_)
         : g(g_), sm(sm_), tid(threadIdx.x), warp(tid >> 5), lane(tid & 31), l8(lane & 7),
@@ -352,31 +432,29 @@ struct Recur {
     }
 
     // local channel of element v of the thread
-    __device__ __forceinline__ int chan(int v) const { return ((v / U) * 8 + l8) * U + v % U; }
-    // Place of a thread's 16 bytes of channels, and of one channel, in a row of the maps: element v of
-    // lane l8 is at (v / Q) 8 Q + l8 Q + v % Q, so that 16-byte accesses of 8 lanes are contiguous; a quarter's
-    // rows are turned by 8 places, so that a scan warp (8 places of four quarters) meets no bank twice.
+    __device__ __forceinline__ int chan(int v) const { return l8 * V + v; }
+    // place of a thread's 16 bytes of channels, and of one channel, in a row of the maps: element v of
+    // lane l8 is at (v / Q) 8 Q + l8 Q + v % Q, so that 16-byte accesses of 8 lanes are contiguous
     static constexpr int Q = 16 / (int)sizeof(A);
-    static __device__ __forceinline__ int turn(int quarter) { return (quarter * 8) & (P::W - 1); }
     static __device__ __forceinline__ int chan_at(int place)
     {
         const int v = place / (8 * Q) * Q + place % Q, l = place / Q % 8;
-        return ((v / U) * 8 + l) * U + v % U;
+        return l * V + v;
     }
-    __device__ __forceinline__ void put_map(A (*m)[P::W], const A (&x)[V]) const
+    __device__ __forceinline__ void put_map(A (&row)[P::W], const A (&x)[V]) const
     {
 #pragma unroll
         for (int j = 0; j < V / Q; ++j) {
             uint4 w;
             memcpy(&w, &x[j * Q], 16);
-            *reinterpret_cast<uint4 *>(&m[run][(j * 8 * Q + l8 * Q) ^ turn(run / P::RQ)]) = w;
+            *reinterpret_cast<uint4 *>(&row[j * 8 * Q + l8 * Q]) = w;
         }
     }
-    __device__ __forceinline__ void get_map(A (*m)[P::W], A (&x)[V]) const
+    __device__ __forceinline__ void get_map(const A (&row)[P::W], A (&x)[V]) const
     {
 #pragma unroll
         for (int j = 0; j < V / Q; ++j) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(&m[run][(j * 8 * Q + l8 * Q) ^ turn(run / P::RQ)]);
+            const uint4 w = *reinterpret_cast<const uint4 *>(&row[j * 8 * Q + l8 * Q]);
             memcpy(&x[j * Q], &w, 16);
         }
     }
@@ -386,74 +464,150 @@ struct Recur {
         return REV ? g.q.n_tokens - 1 - pos : pos;
     }
 
-    __device__ __forceinline__ bool reads(int k) const { return g.in[k] != nullptr; }
+    __device__ __forceinline__ bool reads(int k) const { return k == 0 || !REV || g.in[k] != nullptr; }
 
-    // start the copies of the thread's rows of a tile
-    template <bool SEG>
-    __device__ __forceinline__ void load_rows(const TilePlan &pl, int st)
+    template <int K>
+    __device__ __forceinline__ uint4 *rows_of(int st) const
     {
-        const int64_t c0 = (int64_t)pl.cb * P::W;
-        const int64_t t0 = row_of(pl, p0);
+        return K == 0 ? sm.stage0[st][0] : K == 1 ? sm.stage1[st][0] : sm.stage2[K < 2 ? 0 : K - 2][st][0];
+    }
+    static constexpr bool BOX = UNITS == 1;                // rows go by tensor copies
+    // row of a stage that holds position p: boxes hold rows in memory's order
+    static __device__ __forceinline__ int stage_row(int p) { return BOX && REV ? C - 1 - p : p; }
+
+    // One thread starts the copies of a tile's rows of inputs K0 to K1: whole boxes, in which rows outside the sequences
+    // are not used and rows outside the array are zeros.
+    template <int K0, int K1>
+    __device__ __forceinline__ void copy_boxes(const TilePlan &pl, int j, unsigned long long *bar)
+    {
+        int n = 0;
 #pragma unroll
-        for (int k = 0; k < P::NIN; ++k) {
+        for (int k = K0; k < K1; ++k)
+            n += reads(k) ? 1 : 0;
+        mbar_expect(bar, n * C * 128);
+        const int x = pl.cb * P::W;
+        const int64_t pos = (int64_t)pl.chunk * C;
+#pragma unroll
+        for (int k = K0; k < K1; ++k) {
             if (!reads(k))
                 continue;
-            const int back = REV && k == 2;                // the state before the row
-            const S *src = g.in[k] + (t0 - back) * g.ldin[k] + c0;
-            const int64_t step = REV ? -g.ldin[k] : g.ldin[k];
+            const int y = (int)(REV ? g.q.n_tokens - pos - C : pos) - (REV && k == 2 ? 1 : 0);   // 2: the state before the row
+            void *dst = k == 0 ? rows_of<0>(j % P::NZ) : k == 1 ? rows_of<1>(j % P::N1S) : k == 2 ? rows_of<2>(j % P::NX) : rows_of<3>(j % P::NX);
+            box_in(dst, &g.map[k], x, y, bar);
+        }
+    }
+    // A thread starts the copies of its own values of a tile's rows of input K.
+    template <int K>
+    __device__ __forceinline__ void copy_rows(const TilePlan &pl, int st)
+    {
+        if (!reads(K))
+            return;
+        const int64_t c0 = (int64_t)pl.cb * P::W + l8 * V;
+        constexpr int back = REV && K == 2;                // the state before the row
+        const int64_t t0 = row_of(pl, p0) - back, left = g.n_chan - c0;
+        const S *src = g.in[K] + t0 * g.ldin[K] + c0;
+        const int64_t step = REV ? -g.ldin[K] : g.ldin[K];
 #pragma unroll
-            for (int i = 0; i < R; ++i, src += step) {
-                const int p = p0 + i;
-                if (SEG && (p < pl.lo || p >= pl.hi))
-                    continue;
-                if (back && t0 - i <= 0)
-                    continue;
-                S *dst = reinterpret_cast<S *>(&sm.stage[st][k][i][tid]);
+        for (int i = 0; i < R; ++i, src += step) {
+            const int p = p0 + i;
+            if (p < pl.lo || p >= pl.hi || (back && t0 - i < 0))
+                continue;
+            S *dst = reinterpret_cast<S *>(rows_of<K>(st) + p * 8 + l8);
 #pragma unroll
-                for (int j = 0; j < UNITS; ++j) {
-                    const int c = chan(j * U);
-                    const int64_t left = g.n_chan - c0 - c;
-                    if (left <= 0)
-                        continue;
-                    if constexpr (U * sizeof(S) >= 4)
-                        copy_async<U * (int)sizeof(S)>(dst + j * U, src + c, (int)min(left, (int64_t)U) * (int)sizeof(S));
-                    else
-                        dst[j] = src[c];
-                }
+            for (int u = 0; u < V; u += U) {
+                if (u >= left)
+                    continue;
+                if constexpr (U * sizeof(S) >= 4)
+                    copy_async<U * (int)sizeof(S)>(dst + u, src + u, (int)min(left - u, (int64_t)U) * (int)sizeof(S));
+                else
+                    dst[u] = src[u];
             }
         }
     }
-    __device__ __forceinline__ void load(const TilePlan &pl, int st)
+    // what pass 1 reads of tile j, and what only pass 2 reads: by one thread (BOX) or all compute threads
+    __device__ __forceinline__ void load(const TilePlan &pl, int j)
     {
-        if (pl.tile >= 0) {
-            if (pl.seg)
-                load_rows<true>(pl, st);
-            else
-                load_rows<false>(pl, st);
+        if (pl.tile < 0)
+            return;
+        if constexpr (BOX)
+            copy_boxes<0, 2>(pl, j, &sm.full[j % P::N1S]);
+        else {
+            copy_rows<0>(pl, j % P::NZ);
+            copy_rows<1>(pl, j % P::N1S);
+            mbar_arrive_after_copies(&sm.full[j % P::N1S]);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
     }
-
-    __device__ __forceinline__ void staged(int st, int k, int i, A (&x)[V]) const
+    __device__ __forceinline__ void load_late(const TilePlan &pl, int j)
     {
-        const uint4 r = reads(k) ? sm.stage[st][k][i][tid] : make_uint4(0, 0, 0, 0);
-        unpack16(r, x, S());
+        if constexpr (P::NIN > 2) {
+            if (pl.tile < 0)
+                return;
+            if constexpr (BOX)
+                copy_boxes<2, P::NIN>(pl, j, &sm.late[j % P::NX]);
+            else {
+                copy_rows<2>(pl, j % P::NX);
+                if constexpr (P::NIN > 3)
+                    copy_rows<3>(pl, j % P::NX);
+                mbar_arrive_after_copies(&sm.late[j % P::NX]);
+            }
+        }
+    }
+    // Wait for what load() started.  A barrier that never ended is marked in `lost`, and the rows come out as NaN.
+    __device__ __forceinline__ void loaded(int j)
+    {
+        lost = !mbar_wait(&sm.full[j % P::N1S], j / P::N1S & 1) || lost;
+    }
+    __device__ __forceinline__ void loaded_late(int j)
+    {
+        if constexpr (P::NIN > 2)
+            lost = !mbar_wait(&sm.late[j % P::NX], j / P::NX & 1) || lost;
+    }
+    template <int K>
+    __device__ __forceinline__ void staged(int st, int i, A (&x)[V]) const
+    {
+        unpack16(reads(K) ? rows_of<K>(st)[stage_row(p0 + i) * 8 + l8] : make_uint4(0, 0, 0, 0), x, S());
     }
     __device__ __forceinline__ A enter_of(int s, int64_t ch) const
     {
         return g.enter && ch < g.n_chan ? g.enter[(int64_t)s * g.n_chan + ch] : A(0);
     }
 
-    // (A, H) of the thread's rows
+    // What a thread keeps of its coefficients between the passes: a; of a sigmoid the smaller of a and 1 - a, negative
+    // where that is 1 - a, so that both come back with all their digits.
+    struct Kept {
+        A k[R][V];
+    };
+    static __device__ __forceinline__ void keep(A (&k)[V], const A (&a)[V], const A (&w)[V])
+    {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            k[v] = GATE != SLA_GATE_SIGMOID || a[v] <= w[v] ? a[v] : -w[v];
+    }
+    static __device__ __forceinline__ void kept(const A (&k)[V], A (&a)[V], A (&w)[V])
+    {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if constexpr (GATE == SLA_GATE_SIGMOID) {
+                const A rest = add_of(A(1), k[v] < A(0) ? k[v] : -k[v]);
+                a[v] = k[v] < A(0) ? rest : k[v];
+                w[v] = k[v] < A(0) ? -k[v] : rest;
+            } else {
+                a[v] = k[v];
+                w[v] = A(1);
+            }
+        }
+    }
+
+    // the coefficients and (A, H) of the thread's rows
     template <bool SEG>
-    __device__ __forceinline__ void pass1_rows(const TilePlan &pl, int slot, int st, A (&ma)[V], A (&mh)[V])
+    __device__ __forceinline__ void pass1_rows(const TilePlan &pl, int slot, int sz, int st, Kept &kp, A (&ma)[V], A (&mh)[V])
     {
         const int64_t c0 = (int64_t)pl.cb * P::W;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             A z[V], x[V];
-            staged(st, 0, i, z);
-            staged(st, 1, i, x);
+            staged<0>(sz, i, z);
+            staged<1>(st, i, x);
             const int p = p0 + i;
             int s = -1;
             bool inside = true;
@@ -461,80 +615,125 @@ struct Recur {
                 inside = p >= pl.lo && p < pl.hi;
                 s = inside ? sm.begin[slot][p] : -1;
             }
+            A a[V], w[V], y[V];
+            gates_of<GATE, sizeof(S) == 2>(z, a, w);
+            keep(kp.k[i], a, w);
+            if (SEG && s >= 0)                             // what enters the row by name
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                A a, w;
-                gate_of<GATE, sizeof(S) == 2>(z[v], a, w);
-                A h;
-                if constexpr (!REV) {
-                    const A u = w * x[v];
-                    h = i == 0 ? u : fma_of(a, mh[v], u);
-                    if (SEG && s >= 0)
-                        h = g.enter ? fma_of(a, enter_of(s, c0 + chan(v)), u) : u;
-                } else {
-                    A y = i == 0 ? x[v] : add_of(x[v], mh[v]);
-                    if (SEG && s >= 0)
-                        y = add_of(x[v], enter_of(s, c0 + chan(v)));
-                    h = mul_of(a, y);
+                for (int v = 0; v < V; ++v)
+                    mh[v] = enter_of(s, c0 + chan(v));
+            const bool first = i == 0 && !(SEG && s >= 0);
+            if constexpr (!REV) {
+                if constexpr (GATE == SLA_GATE_SIGMOID)
+                    vmul(x, w, x);
+                if (first || (SEG && s >= 0 && !g.enter))
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        mh[v] = x[v];
+                else
+                    vfma(mh, a, mh, x);
+            } else {
+                if (first)
+                    vmul(mh, a, x);
+                else {
+                    vadd(y, x, mh);
+                    vmul(mh, a, y);
                 }
-                if constexpr (SEG) {
-                    A m = i == 0 ? a + A(0) : product(a, ma[v]);
+            }
+            if constexpr (SEG) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    A m = i == 0 ? a[v] + A(0) : product(a[v], ma[v]);
                     if (s >= 0)
                         m = const_mark<A>();
                     if (!inside) {
                         m = const_mark<A>();
-                        h = A(0);
+                        mh[v] = A(0);
                     }
                     ma[v] = m;
-                } else
-                    ma[v] = i == 0 ? a : i == R - 1 ? ma[v] * a + A(0) : ma[v] * a;
-                mh[v] = h;
-            }
+                }
+            } else if (i == 0)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    ma[v] = a[v];
+            else
+                vmul(ma, ma, a);
+        }
+        if constexpr (!SEG) {                              // -0 marks a constant map
+            A zero[V];
+            vset(zero, A(0));
+            vadd(ma, ma, zero);
         }
     }
 
-    __device__ __forceinline__ void pass1(const TilePlan &pl, int slot, int st, int buf)
+    __device__ __forceinline__ void pass1(const TilePlan &pl, int slot, int sz, int st, int buf, Kept &kp)
     {
         A ma[V], mh[V];
         if (pl.seg)
-            pass1_rows<true>(pl, slot, st, ma, mh);
+            pass1_rows<true>(pl, slot, sz, st, kp, ma, mh);
         else
-            pass1_rows<false>(pl, slot, st, ma, mh);
-        put_map(sm.mapA[buf], ma);
-        put_map(sm.mapH[buf], mh);
+            pass1_rows<false>(pl, slot, sz, st, kp, ma, mh);
+        if (lost)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                mh[v] = A(NAN);
+        put_map(sm.mapA[buf][run], ma);
+        put_map(sm.mapH[buf][run], mh);
     }
 
-    __device__ __forceinline__ void store(int k, int64_t t, int64_t c0, const A (&x)[V])
+    // Row i of the thread's run of output k: to its place in memory, or, where that is not aligned to 16 bytes, to the
+    // place of an input that this thread alone has read (input 1 for output 0, input 2 for output 1), from
+    // where the warp sends whole rows.
+    __device__ __forceinline__ uint4 *out_rows(int k, int st, int sx) const { return k == 0 ? rows_of<1>(st) : rows_of<2>(sx); }
+    __device__ __forceinline__ void store(int k, int i, int64_t t, int64_t c0, int st, int sx, const A (&x)[V])
     {
-        S *dst = g.out[k] + t * g.ldout[k] + c0;
         const uint4 r = pack16(x, S());
-        S s[V];
-        memcpy(s, &r, 16);
+        if constexpr (UNITS > 1)
+            out_rows(k, st, sx)[(p0 + i) * 8 + l8] = r;
+        else {
+            S *dst = g.out[k] + t * g.ldout[k] + c0 + l8 * V;
+            const int64_t left = g.n_chan - c0 - l8 * V;
+            if (left >= V)
+                *reinterpret_cast<uint4 *>(dst) = r;
+            else {
+                S s[V];
+                memcpy(s, &r, 16);
 #pragma unroll
-        for (int j = 0; j < UNITS; ++j) {
-            const int c = chan(j * U);
-            const int64_t left = g.n_chan - c0 - c;
-            if (left >= U) {
-                if constexpr (UNITS == 1)
-                    *reinterpret_cast<uint4 *>(dst + c) = r;
-                else if constexpr (U == 1)
-                    dst[c] = s[j];
-                else {
-                    unsigned w;
-                    memcpy(&w, s + j * U, 4);
-                    *reinterpret_cast<unsigned *>(dst + c) = w;
+                for (int v = 0; v < V; ++v)
+                    if (v < left)
+                        dst[v] = s[v];
+            }
+        }
+    }
+    __device__ __forceinline__ void send_rows(const TilePlan &pl, int st, int sx)
+    {
+        if constexpr (UNITS > 1) {
+            __syncwarp();
+            constexpr int N = P::W / 32;                   // channels of a lane, 32 apart
+            const int64_t c0 = (int64_t)pl.cb * P::W;
+#pragma unroll
+            for (int k = 0; k < (REV ? 2 : 1); ++k) {
+                if (!g.out[k])
+                    continue;
+                const S *src = reinterpret_cast<const S *>(out_rows(k, st, sx) + warp * 16 * 8) + lane;
+#pragma unroll 4
+                for (int r = 0; r < 16; ++r) {
+                    const int p = warp * 16 + r;
+                    const int64_t t = row_of(pl, p);
+                    if ((p >= pl.lo && p < pl.hi) || (g.fill && t >= 0 && t < g.q.n_tokens)) {
+                        S *dst = g.out[k] + t * g.ldout[k] + c0 + lane;
+#pragma unroll
+                        for (int e = 0; e < (N > 0 ? N : 1); ++e)
+                            if (lane + 32 * e < P::W && c0 + lane + 32 * e < g.n_chan)
+                                dst[32 * e] = src[r * P::W + 32 * e];
+                    }
                 }
-            } else if constexpr (U > 1) {
-#pragma unroll
-                for (int e = 0; e < U; ++e)
-                    if (e < left)
-                        dst[c + e] = s[j * U + e];
             }
         }
     }
 
     template <bool SEG>
-    __device__ __forceinline__ void pass2_rows(const TilePlan &pl, int slot, int st, A (&x)[V])
+    __device__ __forceinline__ void pass2_rows(const TilePlan &pl, int slot, int st, int sx, const Kept &kp, A (&x)[V])
     {
         const int64_t c0 = (int64_t)pl.cb * P::W;
 #pragma unroll
@@ -551,56 +750,59 @@ struct Recur {
                             zero[v] = A(0);
                         for (int k = 0; k < (REV ? 2 : 1); ++k)
                             if (g.out[k])
-                                store(k, t, c0, zero);
+                                store(k, i, t, c0, st, sx, zero);
                     }
                     continue;
                 }
                 s = sm.begin[slot][p];
                 f = sm.finish[slot][p];
             }
-            A z[V], y[V];
-            staged(st, 0, i, z);
-            staged(st, 1, i, y);
+            A y[V], a[V], w[V];
+            staged<1>(st, i, y);
+            kept(kp.k[i], a, w);
+            if (SEG && s >= 0)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    x[v] = enter_of(s, c0 + chan(v));
             if constexpr (!REV) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    A a, w;
-                    gate_of<GATE, sizeof(S) == 2>(z[v], a, w);
-                    const A u = w * y[v];
-                    if (SEG && s >= 0)
-                        x[v] = g.enter ? fma_of(a, enter_of(s, c0 + chan(v)), u) : u;
-                    else
-                        x[v] = fma_of(a, x[v], u);
-                }
-                store(0, t, c0, x);
-            } else {
-                A hb[V], u[V], db[V], dz[V];
-                staged(st, 2, i, hb);
                 if constexpr (GATE == SLA_GATE_SIGMOID)
-                    staged(st, 3, i, u);
+                    vmul(y, w, y);
+                if (SEG && s >= 0 && !g.enter)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    A a, w;
-                    gate_of<GATE, sizeof(S) == 2>(z[v], a, w);
-                    const A lam = add_of(y[v], SEG && s >= 0 ? enter_of(s, c0 + chan(v)) : x[v]);
-                    A hp = hb[v];
-                    if (SEG && f >= 0) {
+                    for (int v = 0; v < V; ++v)
+                        x[v] = y[v];
+                else
+                    vfma(x, a, x, y);
+                store(0, i, t, c0, st, sx, x);
+            } else {
+                A hb[V], lam[V];
+                staged<2>(sx, i, hb);
+                if (SEG && f >= 0)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
                         const int64_t ch = c0 + chan(v);
-                        hp = g.before && ch < g.n_chan ? g.before[(int64_t)f * g.n_chan + ch] : A(0);
+                        hb[v] = g.before && ch < g.n_chan ? g.before[(int64_t)f * g.n_chan + ch] : A(0);
                     }
-                    x[v] = mul_of(a, lam);
-                    db[v] = w * lam;
-                    if constexpr (GATE == SLA_GATE_VALUE)
-                        dz[v] = lam * hp;
-                    else if constexpr (GATE == SLA_GATE_EXP)
-                        dz[v] = x[v] * hp;
-                    else
-                        dz[v] = x[v] * w * (hp - u[v]);
-                }
+                vadd(lam, y, x);
+                vmul(x, a, lam);
+                if constexpr (GATE == SLA_GATE_SIGMOID) {
+                    A u[V];
+                    staged<3>(sx, i, u);
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        u[v] = -u[v];
+                    vadd(hb, hb, u);                       // before - b
+                    vmul(lam, w, lam);                     // db
+                    vmul(u, x, w);
+                    vmul(hb, u, hb);
+                } else if constexpr (GATE == SLA_GATE_EXP)
+                    vmul(hb, x, hb);
+                else
+                    vmul(hb, lam, hb);
                 if (g.out[0])
-                    store(0, t, c0, db);
+                    store(0, i, t, c0, st, sx, lam);
                 if (g.out[1])
-                    store(1, t, c0, dz);
+                    store(1, i, t, c0, st, sx, hb);
             }
             if (SEG && f >= 0 && g.leave) {
 #pragma unroll
@@ -613,115 +815,157 @@ struct Recur {
         }
     }
 
-    __device__ __forceinline__ void pass2(const TilePlan &pl, int slot, int st, int buf)
+    __device__ __forceinline__ void pass2(const TilePlan &pl, int slot, int st, int sx, int buf, const Kept &kp)
     {
-        A x[V];
-        get_map(sm.mapH[buf], x);
+        A x[V], a[V], h[V];
+        get_map(sm.mapA[buf][run], a);
+        get_map(sm.mapH[buf][run], h);
+        get_map(sm.enter[buf], x);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            x[v] = apply(a[v], x[v], h[v]);
         if (pl.seg)
-            pass2_rows<true>(pl, slot, st, x);
+            pass2_rows<true>(pl, slot, st, sx, kp, x);
         else
-            pass2_rows<false>(pl, slot, st, x);
+            pass2_rows<false>(pl, slot, st, sx, kp, x);
+        send_rows(pl, st, sx);
     }
 
-    // (A, H) of consecutive runs.  Without borders in the tile no map is constant, and the guard against
-    // an overflowed A times 0 is needed only if a NaN comes out.  The products of four runs stay in fp32
-    // (16 coefficients), longer ones are taken in fp64.
-    template <bool GUARD>
-    static __device__ __forceinline__ void compose(const A (&a)[P::RQ], const A (&h)[P::RQ], double &ta, A &th)
+    // A channel's runs.  In fp32 a map thread holds them all in registers (their loads then pass at once, and the
+    // front maps need no second look); fp64 goes through shared memory twice.
+    static constexpr int HELD = sizeof(A) == 4 ? P::NR : 4;
+    struct Runs {
+        A a[HELD], h[HELD];
+    };
+    __device__ __forceinline__ void take(int buf, int place, int r0, Runs &q) const
     {
-        th = h[0];
 #pragma unroll
-        for (int k = 1; k < P::RQ; ++k)
-            th = GUARD ? apply(a[k], th, h[k]) : fma_of(a[k], th, h[k]);
+        for (int k = 0; k < HELD; ++k) {
+            q.a[k] = sm.mapA[buf][r0 + k][place];
+            q.h[k] = sm.mapH[buf][r0 + k][place];
+        }
+    }
+    // (A, H) of the runs in q behind (ta, th).  PLAIN: no borders in the tile, so no map is constant, and in A's own
+    // type without the guard against an overflowed A times 0; where the tile's result is not finite it is
+    // taken again with both, and with the product in fp64 (of four runs each, 16 coefficients).
+    template <bool PLAIN, typename T>
+    static __device__ __forceinline__ void compose(const Runs &q, T &ta, A &th)
+    {
 #pragma unroll
-        for (int k = 0; k < P::RQ; k += 4) {
-            A m = a[k];
+        for (int k = 0; k < HELD; k += 4) {
 #pragma unroll
-            for (int e = 1; e < 4; ++e)
-                if (k + e < P::RQ)
-                    m = GUARD ? product(a[k + e], m) : a[k + e] * m;
-            if constexpr (GUARD)
-                ta = k ? product((double)m, ta) : (double)m;
+            for (int e = 0; e < 4; ++e)
+                th = PLAIN ? fma_of(q.a[k + e], th, q.h[k + e]) : apply(q.a[k + e], th, q.h[k + e]);
+            if constexpr (PLAIN)
+                ta *= (q.a[k] * q.a[k + 1]) * (q.a[k + 2] * q.a[k + 3]);
             else
-                ta = k ? (double)m * ta : (double)m;
+                ta = product((T)product(product(q.a[k + 3], q.a[k + 2]), product(q.a[k + 1], q.a[k])), ta);
         }
-        if constexpr (!GUARD)
-            ta += 0.0;                                     // -0 marks a constant map
     }
-    // Every run gets the state that enters it.
-    template <bool GUARD>
-    __device__ __forceinline__ void enter_runs(int buf, int r0, int at, const A (&a)[P::RQ], const A (&h)[P::RQ], A x)
+    template <bool PLAIN, typename T>
+    __device__ __forceinline__ void tile_map(int buf, int place, Runs &q, T &ta, A &th) const
     {
-#pragma unroll
-        for (int k = 0; k < P::RQ; ++k) {
-            sm.mapH[buf][r0 + k][at] = x;
-            x = GUARD ? apply(a[k], x, h[k]) : fma_of(a[k], x, h[k]);
+        ta = T(1);
+        th = A(0);
+        for (int r0 = 0; r0 < P::NR; r0 += HELD) {
+            if (HELD < P::NR)
+                take(buf, place, r0, q);
+            compose<PLAIN>(q, ta, th);
         }
+    }
+    // Every run gets the map of the runs in front of it.
+    __device__ __forceinline__ void front_maps(int buf, int place, Runs &q)
+    {
+        A fa = A(1), fh = A(0);
+        for (int r0 = 0; r0 < P::NR; r0 += HELD) {
+            if (HELD < P::NR)
+                take(buf, place, r0, q);
+#pragma unroll
+            for (int k = 0; k < HELD; ++k) {
+                sm.mapA[buf][r0 + k][place] = fa;
+                sm.mapH[buf][r0 + k][place] = fh;
+                fh = fma_of(q.a[k], fh, q.h[k]);
+                fa = fma_of(fa, q.a[k], A(0));             // -0 marks a constant map
+            }
+        }
+    }
+    // Every run gets the constant map of the state that enters it, from x: with borders in the tile, or where
+    // products leave the range.
+    __device__ __forceinline__ void front_states(int buf, int place, A x)
+    {
+#pragma unroll 4
+        for (int r = 0; r < P::NR; ++r) {
+            const A a = sm.mapA[buf][r][place], h = sm.mapH[buf][r][place];
+            sm.mapA[buf][r][place] = const_mark<A>();
+            sm.mapH[buf][r][place] = x;
+            x = apply(a, x, h);
+        }
+    }
+    // whether the runs' maps may be composed in their own type: no borders, everything finite
+    static __device__ __forceinline__ bool plain(const TilePlan &pl, typename Words<A>::Map pa, A th)
+    {
+        return !pl.seg && Words<A>::finite(pa) && isfinite(th);
     }
 
-    // 8 channels of a tile by a warp: publish, find the state that enters, hand it to the runs
-    __device__ __forceinline__ void scan(const TilePlan &pl, int slot, int buf, int sw)
+    // one channel of a tile: its map, published
+    __device__ __forceinline__ void maps(const TilePlan &pl, int buf, int place, Runs &q)
     {
         using Wd = Words<A>;
-        const unsigned all = 0xffffffffu;
-        const int q = lane >> 3, place = sw * 8 + l8, at = place ^ turn(q), r0 = q * P::RQ;
         const int64_t ch = (int64_t)pl.cb * P::W + chan_at(place);
-        const bool real = ch < g.n_chan;
-        A a[P::RQ], h[P::RQ], th, x = A(0);
-        double ta;
-#pragma unroll
-        for (int k = 0; k < P::RQ; ++k) {
-            a[k] = sm.mapA[buf][r0 + k][at];
-            h[k] = sm.mapH[buf][r0 + k][at];
+        A th = A(0);
+        typename Wd::Map pa = Wd::pack(A(1));
+        bool ok = !pl.seg;
+        if (HELD == P::NR)
+            take(buf, place, 0, q);
+        if (ok) {
+            A ta;
+            tile_map<true>(buf, place, q, ta, th);
+            pa = Wd::pack(ta + A(0));
+            ok = isfinite(ta) && isfinite(th);
         }
-        if (pl.seg)
-            compose<true>(a, h, ta, th);
-        else {
-            compose<false>(a, h, ta, th);
-            if (!(th == th))
-                compose<true>(a, h, ta, th);
+        if (!ok) {
+            double ta;
+            tile_map<false>(buf, place, q, ta, th);
+            pa = Wd::pack(ta);
         }
-        const bool plain = !pl.seg && __all_sync(all, isfinite(ta) || !real);
-        // over the quarters; (pa, ph): the quarters in front
-#pragma unroll
-        for (int d = 8; d < 32; d *= 2) {
-            const double oa = __shfl_up_sync(all, ta, d);
-            const A oh = __shfl_up_sync(all, th, d);
-            if (lane >= d) {
-                th = apply_wide(ta, oh, th);
-                ta = product(ta, oa);
-            }
-        }
-        const double pa = __shfl_up_sync(all, ta, 8);
-        const A ph = __shfl_up_sync(all, th, 8);
-        if (g.n_chunks > 1) {
-            ta = Wd::round_a(__shfl_sync(all, ta, 24 + l8));
-            th = __shfl_sync(all, th, 24 + l8);
+        sm.tileA[buf][place] = pa;
+        sm.tileH[buf][place] = th;
+        if (pl.chunk + 1 < g.n_chunks && ch < g.n_chan) {
             const int64_t cell = (int64_t)pl.chunk * g.n_chan + ch;
-            typename Wd::Inc *inc = (typename Wd::Inc *)g.inc;
-            const bool first = pl.chunk == 0, fixed = first || is_const(ta);
-            const bool publish = q == 3 && real && pl.chunk + 1 < g.n_chunks;
-            if (publish) {
-                if (fixed)
-                    st_word(inc + cell, Wd::inc_bits(th));
-                else
-                    Wd::put(g.agg + cell * Wd::N, ta, th);
-            }
-            // a border (or a row outside) at the first position: nothing enters
-            if (!first && !(pl.seg && (pl.lo > 0 || pl.hi == 0 || sm.begin[slot][0] >= 0))) {
-                x = state_before<A>(pl.chunk, g.n_chan, ch, real, lane, g.agg, inc);
-                if (publish && !fixed)
-                    st_word(inc + cell, Wd::inc_bits(apply_wide(ta, x, th)));
-            }
+            if (pl.chunk == 0 || Wd::fixed(pa))
+                st_word((typename Wd::Inc *)g.inc + cell, Wd::inc_bits(th));
+            else
+                Wd::put(g.agg + cell * Wd::N, pa, th);
         }
-        if (q > 0)
-            x = apply_wide(pa, x, ph);
-        // The guard is needed with constant maps, and where a run's A overflowed, which leaves its quarter's
-        // not finite.
-        if (plain)
-            enter_runs<false>(buf, r0, at, a, h, x);
-        else
-            enter_runs<true>(buf, r0, at, a, h, x);
+    }
+
+    // whether the state before the tile is needed: not where a border (or a row outside) is at its first position
+    __device__ __forceinline__ bool enters(const TilePlan &pl, int slot) const
+    {
+        return pl.chunk > 0 && !(pl.seg && (pl.lo > 0 || pl.hi == 0 || sm.begin[slot][0] >= 0));
+    }
+    // one channel of a tile: the state that enters it
+    __device__ __forceinline__ A find_state(const TilePlan &pl, int slot, int place) const
+    {
+        const int64_t ch = (int64_t)pl.cb * P::W + chan_at(place);
+        if (ch >= g.n_chan || !enters(pl, slot))
+            return A(0);
+        return state_before<A>(pl.chunk, g.n_chan, ch, g.n_cb * 4 < (int)gridDim.x, g.agg, (const typename Words<A>::Inc *)g.inc);
+    }
+    // its leaving state, published, and where the maps do not compose the runs' states
+    __device__ __forceinline__ void hand_over(const TilePlan &pl, int slot, int buf, int place, A x)
+    {
+        using Wd = Words<A>;
+        const int64_t ch = (int64_t)pl.cb * P::W + chan_at(place);
+        const typename Wd::Map pa = sm.tileA[buf][place];
+        const A th = sm.tileH[buf][place];
+        sm.enter[buf][place] = x;
+        if (ch >= g.n_chan)
+            return;
+        if (pl.chunk + 1 < g.n_chunks && !Wd::fixed(pa) && enters(pl, slot))
+            st_word((typename Wd::Inc *)g.inc + (int64_t)pl.chunk * g.n_chan + ch, Wd::inc_bits(Wd::apply(pa, x, th)));
+        if (!plain(pl, pa, th))
+            front_states(buf, place, x);
     }
 
     // the plan warp: the next tile, and where sequences begin and end in it
@@ -799,69 +1043,122 @@ struct Recur {
     }
 };
 
-constexpr int BAR_P1 = 1, BAR_P2 = 3, BAR_PLAN = 5;
+// Barriers, each with the warps that arrive and those that wait, one for each of the two tiles at hand: the
+// runs' maps are there (compute -> map), the tile's map is there (map -> state), and the front maps, the
+// entering states and the plan NS tiles ahead are there (map, state, plan -> compute, plan).
+constexpr int BAR_RUNS = 1, BAR_TILE = 3, BAR_ENTER = 5, BAR_START = 7, BAR_FIRST = 8;
 
 template <typename S, int GATE, int U, bool REV>
 __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const __grid_constant__ RecurArgs<S> g)
 {
     using P = RecurShape<S, GATE, REV>;
     using A = typename RowType<S>::A;
+    using K = Recur<S, GATE, U, REV>;
     constexpr int NS = P::NS, NP = P::NP;
-    extern __shared__ __align__(16) unsigned char smem_raw[];
+    extern __shared__ __align__(128) unsigned char smem_raw[];
     RecurSmem<S, GATE, REV> &sm = *reinterpret_cast<RecurSmem<S, GATE, REV> *>(smem_raw);
-    Recur<S, GATE, U, REV> r(g, sm);
+    K r(g, sm);
+    constexpr int RUNS = P::NC + P::NK, TILE = 2 * P::NK, ENTER = P::NC + 2 * P::NK + 32, START = P::NC + 32;
+    auto up = [](int x, int n) { return x + 1 == n ? 0 : x + 1; };
+    const int place = (r.tid - P::NC) % P::NK;             // of map and state threads
 
     if (r.tid < P::NC) {                                   // compute warps
-        for (int j = 0; j < NS; ++j) {
-            bar_sync(BAR_PLAN, P::NC + 32);
-            r.load(sm.plan[j], j);
-            __syncwarp();
+        typename K::Kept now, next;
+        bar_sync(BAR_FIRST, P::NT);                        // plan 0
+        if constexpr (!K::BOX) {
+            r.load(sm.plan[0], 0);
+            r.load_late(sm.plan[0], 0);
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(NS - 1) : "memory");
-        if (sm.plan[0].tile >= 0)
-            r.pass1(sm.plan[0], 0, 0, 0);
+        if (sm.plan[0].tile >= 0) {
+            r.loaded(0);
+            r.pass1(sm.plan[0], 0, 0, 0, 0, now);
+        }
         __syncwarp();
-        bar_arrive(BAR_P1, P::NC + P::NSCAN);
-        int st = 0, slot = 0, buf = 0;
-        while (sm.plan[slot].tile >= 0) {
-            const int st1 = st + 1 == NS ? 0 : st + 1, slot1 = slot + 1 == NP ? 0 : slot + 1;
-            asm volatile("cp.async.wait_group %0;" ::"n"(NS - 2) : "memory");
-            if (sm.plan[slot1].tile >= 0)
-                r.pass1(sm.plan[slot1], slot1, st1, buf ^ 1);
-            __syncwarp();
-            bar_arrive(BAR_P1 + (buf ^ 1), P::NC + P::NSCAN);
-            bar_sync(BAR_P2 + buf, P::NC + P::NSCAN);
-            r.pass2(sm.plan[slot], slot, st, buf);
-            __syncwarp();
-            bar_sync(BAR_PLAN, P::NC + 32);
-            const int ahead = slot + NS >= NP ? slot + NS - NP : slot + NS;
-            r.load(sm.plan[ahead], st);
-            st = st1;
-            slot = slot1;
-            buf ^= 1;
+        bar_arrive(BAR_RUNS, RUNS);
+        for (int j = 1; j < NS; ++j) {
+            bar_sync(BAR_START, START);                    // the plans of the next tiles
+            if constexpr (!K::BOX) {
+                r.load(sm.plan[j], j);
+                if (j == 1)
+                    r.load_late(sm.plan[1], 1);
+                __syncwarp();
+            }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        int slot = 0;
+        for (int i = 0; sm.plan[slot].tile >= 0; ++i) {
+            const int slot1 = up(slot, NP), odd = i & 1;
+            if (sm.plan[slot1].tile >= 0) {
+                r.loaded(i + 1);
+                r.pass1(sm.plan[slot1], slot1, (i + 1) % P::NZ, (i + 1) % P::N1S, odd ^ 1, next);
+            }
+            __syncwarp();
+            bar_arrive(BAR_RUNS + (odd ^ 1), RUNS);        // the first tile there is none of ends the map warps
+            bar_sync(BAR_ENTER + odd, ENTER);
+            r.loaded_late(i);
+            r.pass2(sm.plan[slot], slot, i % P::N1S, i % P::NX, odd, now);
+            if constexpr (!K::BOX) {
+                const int slot2 = up(slot1, NP);
+                r.load(sm.plan[up(slot2, NP)], i + 3);
+                r.load_late(sm.plan[slot2], i + 2);
+            }
+            now = next;
+            __syncwarp();
+            slot = slot1;
+        }
+        if constexpr (!K::BOX)
+            asm volatile("cp.async.wait_all;" ::: "memory");
         // empty sequences leave with what entered them
         if (g.leave)
             for (int64_t s = blockIdx.x; s < g.q.n_seq; s += gridDim.x)
                 if (g.q.at(s + 1) <= g.q.at(s))
                     for (int64_t c = r.tid; c < g.n_chan; c += P::NC)
                         g.leave[s * g.n_chan + c] = g.enter ? g.enter[s * g.n_chan + c] : A(0);
-    } else if (r.tid < P::NC + P::NSCAN) {                 // scan warps
-        int slot = 0, buf = 0;
-        for (;;) {
-            bar_sync(BAR_P1 + buf, P::NC + P::NSCAN);
-            if (sm.plan[slot].tile < 0)
+    } else if (r.tid < P::NC + P::NK) {                    // map warps
+        bar_sync(BAR_FIRST, P::NT);
+        for (int slot = 0, odd = 0;; slot = up(slot, NP), odd ^= 1) {
+            bar_sync(BAR_RUNS + odd, RUNS);
+            const TilePlan &pl = sm.plan[slot];
+            if (pl.tile < 0)
                 break;
-            r.scan(sm.plan[slot], slot, buf, r.warp - P::NW);
+            typename K::Runs q;
+            if (place < P::W)
+                r.maps(pl, odd, place, q);
             __syncwarp();
-            bar_arrive(BAR_P2 + buf, P::NC + P::NSCAN);
-            slot = slot + 1 == NP ? 0 : slot + 1;
-            buf ^= 1;
+            bar_arrive(BAR_TILE + odd, TILE);
+            if (place < P::W && K::plain(pl, sm.tileA[odd][place], sm.tileH[odd][place]))
+                r.front_maps(odd, place, q);
+            __syncwarp();
+            bar_arrive(BAR_ENTER + odd, ENTER);
+        }
+    } else if (r.tid < P::NC + 2 * P::NK) {                // state warps
+        bar_sync(BAR_FIRST, P::NT);
+        for (int slot = 0, odd = 0;; slot = up(slot, NP), odd ^= 1) {
+            const TilePlan &pl = sm.plan[slot];            // there since the barriers of the tile before
+            if (pl.tile < 0)
+                break;
+            A x = A(0);
+            if (place < P::W)
+                x = r.find_state(pl, slot, place);
+            __syncwarp();
+            bar_sync(BAR_TILE + odd, TILE);
+            if (place < P::W)
+                r.hand_over(pl, slot, odd, place, x);
+            __syncwarp();
+            bar_arrive(BAR_ENTER + odd, ENTER);
         }
     } else {                                               // plan warp
-        // the compute warps take NS plans before their loop and one in every turn of it
-        int slot = 0, end = INT32_MAX;
+        // The compute warps take NS plans before their loop and one in every turn of it, when they are done with the
+        // tile before and with pass 1 of the next one: the stages of tile j are free.
+        int slot = 0, end = INT32_MAX, odd = 0;
+        if (r.lane == 0) {
+            for (int m = 0; m < P::N1S; ++m)
+                mbar_init(&sm.full[m], K::BOX ? 1 : P::NC);
+            for (int m = 0; m < P::NX; ++m)
+                mbar_init(&sm.late[m], K::BOX ? 1 : P::NC);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
         for (int j = 0; j < end; ++j) {
             if (end == INT32_MAX) {
                 if (!r.plan(slot, j))
@@ -869,8 +1166,21 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
             } else if (r.lane == 0)
                 sm.plan[slot].tile = -1;
             __syncwarp();
-            bar_sync(BAR_PLAN, P::NC + 32);
-            slot = slot + 1 == NP ? 0 : slot + 1;
+            if (j == 0)
+                bar_sync(BAR_FIRST, P::NT);
+            else if (j < NS)
+                bar_sync(BAR_START, START);
+            else {
+                bar_sync(BAR_ENTER + odd, ENTER);
+                odd ^= 1;
+            }
+            if (K::BOX && r.lane == 0) {
+                r.load(sm.plan[slot], j);
+                if (j >= 2)
+                    r.load_late(sm.plan[slot >= 2 ? slot - 2 : slot + NP - 2], j - 2);
+            }
+            __syncwarp();
+            slot = up(slot, NP);
         }
     }
 }
@@ -899,20 +1209,52 @@ sla_status launch_recur_u(RecurArgs<S> &g, cudaStream_t s)
     return SLA_SUCCESS;
 }
 
-// The widest unit of channels that every array's rows are aligned to: 16 bytes, 4 bytes (two of a 16-bit
-// type) or one value.  Copies below 4 bytes are not asynchronous.
+// cuTensorMapEncodeTiled, looked up once (the library does not link against the driver); NULL if there is none.
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled();
+
+// Rows as boxes of `rows` times 128 bytes.
+template <typename S>
+bool box_map(CUtensorMap *map, const S *p, int64_t n_tokens, int64_t n_chan, int64_t ld, int rows)
+{
+    const CUtensorMapDataType type = std::is_same<S, float>::value    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : std::is_same<S, double>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT64
+                                     : std::is_same<S, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint64_t dims[2] = {(cuuint64_t)n_chan, (cuuint64_t)n_tokens}, strides[1] = {(cuuint64_t)ld * sizeof(S)};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / sizeof(S)), (cuuint32_t)rows}, each[2] = {1, 1};
+    return encode_tiled()(map, type, 2, (void *)p, dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// By alignment: tensor copies where every array's rows are aligned to 16 bytes and every input has a stride (a row
+// expanded over the tokens has none); else units of 4 bytes (two of a 16-bit type) or one value.  Copies
+// below 4 bytes are not asynchronous.
 template <typename S, int GATE, bool REV>
 sla_status launch_recur(RecurArgs<S> &g, cudaStream_t s)
 {
+    using P = RecurShape<S, GATE, REV>;
     uintptr_t bits = 0;
+    bool strides = encode_tiled() != nullptr && g.q.n_tokens > 0;
     for (int k = 0; k < 4; ++k)
-        if (g.in[k])
+        if (g.in[k]) {
             bits |= (uintptr_t)g.in[k] | (uintptr_t)(g.ldin[k] * (int64_t)sizeof(S));
+            strides = strides && g.ldin[k] > 0 && g.ldin[k] < (int64_t)1 << 36;
+        }
     for (int k = 0; k < 2; ++k)
         if (g.out[k])
             bits |= (uintptr_t)g.out[k] | (uintptr_t)(g.ldout[k] * (int64_t)sizeof(S));
-    if (bits % 16 == 0)
-        return launch_recur_u<S, GATE, 16 / (int)sizeof(S), REV>(g, s);
+    if (bits % 16 == 0 && strides) {
+        bool ok = true;
+        for (int k = 0; k < 4; ++k)
+            if (g.in[k])
+                ok = ok && box_map<S>(&g.map[k], g.in[k], g.q.n_tokens, g.n_chan, g.ldin[k], P::C);
+        if (ok)
+            return launch_recur_u<S, GATE, 16 / (int)sizeof(S), REV>(g, s);
+    }
     if constexpr (sizeof(S) == 2)
         if (bits % 4 == 0)
             return launch_recur_u<S, GATE, 2, REV>(g, s);

@@ -125,47 +125,148 @@ __device__ __forceinline__ uint4 pack16(const float (&x)[8], __half)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// exp and 1 / (1 + e) of a gate.  Rows of 16 bits take the hardware's exp2 directly (2^-22 relative and
-// 2^-24 |x log2 e| from rounding its argument): z itself was rounded by 2^-9 |z| (bf16) or 2^-12 |z| (fp16),
-// so its coefficient is already uncertain by over 100 times that, and the exact function's extra
-// instructions would show at one pass over memory.  The hardware's reciprocal is 2^-23 relative.
-template <bool FAST>
-__device__ __forceinline__ float gate_exp(float x)
+// Arithmetic on a thread's N values; fp32 in pairs, one instruction for two (rounded as the single ones).
+template <int N>
+__device__ __forceinline__ void vfma(float (&d)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N])
 {
-    if constexpr (FAST) {
-        float r;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
-        return r;
-    } else
-        return expf(x);
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+        asm("{ .reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+            "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d; }"
+            : "=f"(d[i]), "=f"(d[i + 1])
+            : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]), "f"(c[i]), "f"(c[i + 1]));
 }
-template <bool FAST>
-__device__ __forceinline__ double gate_exp(double x) { return exp(x); }
-__device__ __forceinline__ float gate_rcp(float x)
+template <int N>
+__device__ __forceinline__ void vmul(float (&d)[N], const float (&a)[N], const float (&b)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+        asm("{ .reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+            "mov.b64 {%0, %1}, d; }"
+            : "=f"(d[i]), "=f"(d[i + 1])
+            : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+}
+template <int N>
+__device__ __forceinline__ void vadd(float (&d)[N], const float (&a)[N], const float (&b)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 2)
+        asm("{ .reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
+            "mov.b64 {%0, %1}, d; }"
+            : "=f"(d[i]), "=f"(d[i + 1])
+            : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+}
+template <int N>
+__device__ __forceinline__ void vfma(double (&d)[N], const double (&a)[N], const double (&b)[N], const double (&c)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        d[i] = __fma_rn(a[i], b[i], c[i]);
+}
+template <int N>
+__device__ __forceinline__ void vmul(double (&d)[N], const double (&a)[N], const double (&b)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        d[i] = __dmul_rn(a[i], b[i]);
+}
+template <int N>
+__device__ __forceinline__ void vadd(double (&d)[N], const double (&a)[N], const double (&b)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        d[i] = __dadd_rn(a[i], b[i]);
+}
+template <typename A, int N>
+__device__ __forceinline__ void vset(A (&d)[N], A x)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        d[i] = x;
+}
+
+__device__ __forceinline__ float ex2_approx(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// the hardware's reciprocal, 2^-23 relative
+__device__ __forceinline__ float rcp_of(float x)
 {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ double gate_rcp(double x) { return 1.0 / x; }
+__device__ __forceinline__ double rcp_of(double x) { return 1.0 / x; }
 
-// Coefficient a and input weight w of a stored gate value z.  Both halves of the sigmoid come from
-// one e = exp(-z), a = 1 / (1 + e) and w = e a, so that 1 - a keeps its digits where a rounds to 1.  z
-// is held above -86 (fp64: -700), where e would leave the range and a is below 1e-37 anyway.
-template <int GATE, bool FAST, typename A>
-__device__ __forceinline__ void gate_of(A z, A &a, A &w)
+// Coefficients a and input weights w of stored gate values z.
+//
+// exp: rows of 16 bits take the hardware's exp2 (2^-22 relative), except near 0, where a coefficient near 1 carries
+// a state over 1 / |z| rows and its error counts as often: there 1 + z (1 + z/2 + ... + z^5/720), whose
+// truncation at |z| = 1/4 is 2^-26 and whose error is the rounding of the last sum.
+//
+// sigmoid: both halves come from one e = exp(-z), a = 1 / (1 + e) and w = e a, so that 1 - a keeps its digits where
+// a rounds to 1.  z is held above -86 (fp64: -700), where e would leave the range and a is below 1e-37
+// anyway.  An error of e counts 1 - a times in a, so the plain exp2 is enough for 16-bit rows.
+template <int GATE, bool FAST, typename A, int N>
+__device__ __forceinline__ void gates_of(const A (&z)[N], A (&a)[N], A (&w)[N])
 {
     if constexpr (GATE == SLA_GATE_VALUE) {
-        a = z;
-        w = A(1);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            a[i] = z[i];
+        vset(w, A(1));
     } else if constexpr (GATE == SLA_GATE_EXP) {
-        a = gate_exp<FAST>(z);
-        w = A(1);
+        vset(w, A(1));
+        if constexpr (FAST) {
+            float t[N], q[N], c[N];
+            vset(c, 1.4426950408889634f);
+            vmul(t, z, c);
+            vset(q, 1.0f / 720.0f);
+            vset(c, 1.0f / 120.0f);
+            vfma(q, z, q, c);
+            vset(c, 1.0f / 24.0f);
+            vfma(q, z, q, c);
+            vset(c, 1.0f / 6.0f);
+            vfma(q, z, q, c);
+            vset(c, 0.5f);
+            vfma(q, z, q, c);
+            vset(c, 1.0f);
+            vfma(q, z, q, c);
+            vfma(q, z, q, c);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                a[i] = fabsf(z[i]) < 0.25f ? q[i] : ex2_approx(t[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                a[i] = exp(z[i]);
+        }
     } else {
-        const A floor = sizeof(A) == 4 ? A(-86) : A(-700);
-        const A e = gate_exp<FAST>(-(z < floor ? floor : z));   // a NaN stays one
-        a = gate_rcp(A(1) + e);
-        w = e * a;
+        A e[N];
+        if constexpr (FAST) {
+            float c[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                e[i] = z[i] < -86.0f ? -86.0f : z[i];      // a NaN stays one
+            vset(c, -1.4426950408889634f);
+            vmul(e, e, c);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                e[i] = ex2_approx(e[i]);
+        } else {
+            const A floor = sizeof(A) == 4 ? A(-86) : A(-700);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                e[i] = exp(-(z[i] < floor ? floor : z[i]));
+        }
+        vset(a, A(1));
+        vadd(a, a, e);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            a[i] = rcp_of(a[i]);
+        vmul(w, e, a);
     }
 }
 
