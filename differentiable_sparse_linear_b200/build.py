@@ -1,4 +1,5 @@
-"""Build libsla.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a.
+"""Build libsla.so (the C-ABI CUDA library) in-tree with nvcc for sm_100a, and _sla_seq.so, the torch
+side of the sequence operators (g++, linked against libsla.so and the installed torch).
 
 Each .cu file under csrc/ is compiled to an object with
 ``-gencode arch=compute_100a,code=sm_100a -lineinfo -O3`` and the objects are linked into
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libsla.so")
+SEQ_SRC = os.path.join(CSRC, "seq_binding.cpp")
+SEQ_LIB = os.path.join(LIBDIR, "_sla_seq.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -72,7 +76,33 @@ def build(verbose: bool = False, force: bool = False, extra: tuple[str, ...] = (
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    build_seq(verbose=verbose, force=force)
     return LIB
+
+
+def build_seq(verbose: bool = False, force: bool = False) -> str:
+    """_sla_seq.so: rebuilt when its source, the header or the installed torch is newer."""
+    import torch
+    from torch.utils import cpp_extension
+    newest = max(os.path.getmtime(p) for p in (SEQ_SRC, os.path.join(INCLUDE, "sla.h"), __file__, torch.__file__))
+    if not force and os.path.exists(SEQ_LIB) and os.path.getmtime(SEQ_LIB) >= newest:
+        return SEQ_LIB
+    tmp = SEQ_LIB + f".tmp{os.getpid()}"
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include")]
+    for path in cpp_extension.include_paths():
+        cmd += ["-isystem", path]
+    cmd += [SEQ_SRC, "-o", tmp, "-L", LIBDIR, "-Wl,-rpath,$ORIGIN", "-lsla"]
+    for path in cpp_extension.library_paths():
+        cmd += ["-L", path]
+    cmd += ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, SEQ_LIB)
+    return SEQ_LIB
 
 
 if __name__ == "__main__":

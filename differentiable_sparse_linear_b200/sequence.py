@@ -22,7 +22,8 @@ graph still holds makes torch's engine join that graph's stream, which a capture
 """
 from __future__ import annotations
 
-import functools
+import importlib.util
+import os
 from dataclasses import dataclass
 from typing import Optional
 
@@ -39,149 +40,52 @@ __all__ = [
 
 # what the stored coefficients hold (SLA_GATE_*): the value, its logarithm, or a sigmoid's argument
 GATES = {"value": 0, "exp": 1, "sigmoid": 2}
-_ROW_CODES = {torch.float32: _lib.SLA_F32, torch.float64: _lib.SLA_F64, torch.bfloat16: _lib.SLA_BF16,
-              torch.float16: _lib.SLA_F16}
+
+NATIVE_PATH = os.path.join(_lib.PKG, "lib", "_sla_seq.so")
+_native = None
 
 
-def _check(status: int, where: str) -> None:
-    if status < 0:
+def _load():
+    """The native side (csrc/seq_binding.cpp): checks, allocation and the library call.  Loaded at first use;
+    there is no other path."""
+    global _native
+    if _native is None:
+        _lib.load()
+        if not os.path.exists(NATIVE_PATH):
+            raise ImportError(f"_sla_seq.so not found at {NATIVE_PATH}: build it with "
+                              "`python -m differentiable_sparse_linear_b200.build`")
+        spec = importlib.util.spec_from_file_location("_sla_seq", NATIVE_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
         from . import SlaError
-        raise SlaError(status, where)
+        module.set_error_types(SlaError, torch.OutOfMemoryError)
+        _native = module
+    return _native
 
 
-def _placed(fn):
-    """Runs fn with its first tensor's device current, on that device's current stream or on `stream`."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        first = args[0] if args else next(iter(kw.values()), None)
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise ValueError("libsla takes CUDA tensors")
-        device = first.device
-        if stream is None and device.index == torch.cuda.current_device():
-            return fn(*args, **kw)
-        with torch.cuda.device(device):
-            if stream is None:
-                return fn(*args, **kw)
-            if not isinstance(stream, torch.cuda.Stream):
-                handle = int(getattr(stream, "cuda_stream", stream))
-                stream = (torch.cuda.ExternalStream(handle, device=device) if handle
-                          else torch.cuda.default_stream(device))
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-            with torch.cuda.stream(stream):
-                return fn(*args, **kw)
-    return call
-
-
-def _current(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _code(t: torch.Tensor) -> int:
-    code = _ROW_CODES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"rows must be float32, float64, bfloat16 or float16, got {t.dtype}")
-    return code
-
-
-def _wide(dtype: torch.dtype) -> torch.dtype:
-    return torch.float64 if dtype == torch.float64 else torch.float32
-
-
-def _gate(gate: str) -> int:
-    code = GATES.get(gate)
-    if code is None:
-        raise ValueError(f"gate must be one of {sorted(GATES)}, got {gate!r}")
-    return code
-
-
-def _stride(t: torch.Tensor) -> Optional[int]:
-    """The one stride that walks t's rows ([rows, channels] or [batch, rows, channels]); None if
-    there is none."""
-    shape, strides = t.shape, t.stride()
-    d = shape[-1]
-    if d > 1 and strides[-1] != 1:
-        return None
-    if len(shape) == 3:
-        if shape[0] == 1 or shape[1] == 1:
-            ld, n = (strides[1], shape[1]) if shape[0] == 1 else (strides[0], shape[0])
-        else:
-            ld, n = strides[1], 2
-            if strides[0] != shape[1] * ld:
-                return None
-    else:
-        ld, n = strides[0], shape[0]
-    if n <= 1:
-        return d
-    return ld if ld >= d or ld == 0 else None
-
-
-def _rows(t: torch.Tensor, like: torch.Tensor, name: str, out: bool = False) -> int:
-    """Checks rows `t` against `like` (shape, type, device); their row stride."""
-    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} must be {tuple(like.shape)} {like.dtype} on {like.device}, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    ld = _stride(t)
-    if ld is None:
-        raise ValueError(f"{name}: channels must be contiguous and rows one stride apart")
-    if out and ld < t.shape[-1]:
-        raise ValueError(f"{name}: an output's rows must not overlap")
-    return ld
-
-
-def _plain(t: Optional[torch.Tensor], shape, dtype, device, name: str) -> Optional[int]:
-    """Checks a contiguous tensor; its pointer (None for None)."""
-    if t is None:
-        return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {device}, got {tuple(t.shape)} {t.dtype} "
-                         f"on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _on(stream, tensor: torch.Tensor):
+    """`stream` (a torch stream or a handle) as the current stream of the tensor's device."""
+    if not isinstance(tensor, torch.Tensor) or not tensor.is_cuda:
+        raise ValueError("libsla takes CUDA tensors")
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        stream = (torch.cuda.ExternalStream(handle, device=tensor.device) if handle
+                  else torch.cuda.default_stream(tensor.device))
+    if stream.device != tensor.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {tensor.device}")
+    return torch.cuda.stream(stream)
 
 
 def _walkable(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     """t, or a contiguous copy where no single stride walks its rows."""
-    return t if t is None or _stride(t) is not None else t.contiguous()
-
-
-def _sequences(b: torch.Tensor, seq_off: Optional[torch.Tensor]):
-    """(tokens, channels, sequences, offsets pointer) of rows b."""
-    if b.dim() == 3:
-        if seq_off is not None:
-            raise ValueError("seq_off goes with packed [tokens, channels] rows")
-        return b.shape[0] * b.shape[1], b.shape[2], b.shape[0], None
-    if b.dim() != 2:
-        raise ValueError("rows must be [tokens, channels] or [batch, tokens, channels]")
-    if seq_off is None:
-        return b.shape[0], b.shape[1], 1, None
-    if (seq_off.dtype != torch.int32 or seq_off.dim() != 1 or seq_off.numel() < 1 or seq_off.device != b.device
-            or not seq_off.is_contiguous()):
-        raise ValueError("seq_off must be a contiguous int32 vector on the rows' device")
-    return b.shape[0], b.shape[1], seq_off.numel() - 1, seq_off.data_ptr()
-
-
-@functools.lru_cache(maxsize=256)
-def _recur_work(code: int, tokens: int, channels: int) -> int:
-    return _lib.load().sla_recur_workspace_bytes(code, tokens, channels)
-
-
-@functools.lru_cache(maxsize=256)
-def _route_work(tokens: int, top_k: int, experts: int) -> int:
-    return _lib.load().sla_route_workspace_bytes(tokens, top_k, experts)
-
-
-def _scratch(size: int, device: torch.device):
-    return torch.empty(size, dtype=torch.uint8, device=device) if size else None
+    return t if t is None or _load().stride_of(t) is not None else t.contiguous()
 
 
 # ------------------------------------------------------------------------------ recurrence
 
-@_placed
 def sla_recur_solve(a: torch.Tensor, b: torch.Tensor, h0: Optional[torch.Tensor] = None,
                     seq_off: Optional[torch.Tensor] = None, *, gate: str = "value",
-                    out: Optional[torch.Tensor] = None, h_last: Optional[torch.Tensor] = None):
+                    out: Optional[torch.Tensor] = None, h_last: Optional[torch.Tensor] = None, stream=None):
     """h_t = a_t h_{t-1} + w_t b_t over every sequence; returns (h, last states).
 
     a, b: [tokens, channels] packed rows, sequence s owning rows seq_off[s] to seq_off[s + 1] (int32,
@@ -189,101 +93,39 @@ def sla_recur_solve(a: torch.Tensor, b: torch.Tensor, h0: Optional[torch.Tensor]
     gate: what a holds ("value": a itself; "exp": its logarithm; "sigmoid": a = sigmoid, and the
     input is weighted by 1 - a).  h0: [sequences, channels] first states (None: zero).  Rows in no
     sequence come back as zeros, or, with `out` given, as they were."""
-    code, g = _code(b), _gate(gate)
-    tokens, channels, seqs, off = _sequences(b, seq_off)
-    lda, ldb = _rows(a, b, "a"), _rows(b, b, "b")
-    wide, device = _wide(b.dtype), b.device
-    p0 = _plain(h0, (seqs, channels), wide, device, "h0")
-    flags = 0
-    if out is None:
-        out, ldh, flags = torch.empty(b.shape, dtype=b.dtype, device=device), channels, _lib.SLA_FILL_REST
-    else:
-        ldh = _rows(out, b, "out", out=True)
-    if h_last is None:
-        h_last = torch.empty((seqs, channels), dtype=wide, device=device)
-    size = _recur_work(code, tokens, channels)
-    work = _scratch(size, device)
-    _check(_lib.load().sla_recur_solve(
-        code, g, tokens, channels, seqs, off, a.data_ptr(), lda, b.data_ptr(), ldb, p0, out.data_ptr(), ldh,
-        _plain(h_last, (seqs, channels), wide, device, "h_last"), flags,
-        None if work is None else work.data_ptr(), size, _current(device)), "sla_recur_solve")
-    return out, h_last
+    if stream is not None:
+        with _on(stream, b):
+            return _load().recur_solve(a, b, h0, seq_off, gate, out, h_last)
+    return (_native or _load()).recur_solve(a, b, h0, seq_off, gate, out, h_last)
 
 
-@_placed
 def sla_recur_adjoint(a: torch.Tensor, h: torch.Tensor, dh: Optional[torch.Tensor], *,
                       b: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
                       seq_off: Optional[torch.Tensor] = None, dh_last: Optional[torch.Tensor] = None,
                       gate: str = "value", want_da: bool = True, want_db: bool = True,
-                      da: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None):
+                      da: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None, stream=None):
     """Adjoint of sla_recur_solve: (dL/da, dL/db, dL/dh0) from dh = dL/dh and dh_last = dL/d(last
     states), either of them None for zero.  h: the rows the solve returned; a, h0, seq_off, gate: as
     there; b: its inputs, which the sigmoid gate's dL/da needs.  dL/da is with respect to what a
     holds.  Skipped gradients (want_da, want_db; dL/dh0 without h0) are None; rows in no sequence
     have zero gradients (with `da`, `db` given they stay as they were)."""
-    code, g = _code(h), _gate(gate)
-    tokens, channels, seqs, off = _sequences(h, seq_off)
-    lda, ldh = _rows(a, h, "a"), _rows(h, h, "h")
-    wide, device = _wide(h.dtype), h.device
-    if gate == "sigmoid" and want_da:
-        if b is None:
-            raise ValueError("the sigmoid gate's gradient needs b")
-        pb, ldb = b, _rows(b, h, "b")
-    else:
-        pb, ldb = None, 0
-    lddh = 0 if dh is None else _rows(dh, h, "dh")
-    p0 = _plain(h0, (seqs, channels), wide, device, "h0")
-    plast = _plain(dh_last, (seqs, channels), wide, device, "dh_last")
-    flags = 0
-    if da is None and db is None:
-        flags = _lib.SLA_FILL_REST
-        da = torch.empty(h.shape, dtype=h.dtype, device=device) if want_da else None
-        db = torch.empty(h.shape, dtype=h.dtype, device=device) if want_db else None
-    elif (want_da and da is None) or (want_db and db is None):
-        raise ValueError("give both da and db, or neither")
-    ldda = _rows(da, h, "da", out=True) if want_da else 0
-    lddb = _rows(db, h, "db", out=True) if want_db else 0
-    dh0 = None if h0 is None else torch.empty((seqs, channels), dtype=wide, device=device)
-    size = _recur_work(code, tokens, channels)
-    work = _scratch(size, device)
-    _check(_lib.load().sla_recur_adjoint(
-        code, g, tokens, channels, seqs, off, a.data_ptr(), lda, None if pb is None else pb.data_ptr(), ldb,
-        h.data_ptr(), ldh, p0, None if dh is None else dh.data_ptr(), lddh, plast,
-        da.data_ptr() if want_da else None, ldda, db.data_ptr() if want_db else None, lddb,
-        None if dh0 is None else dh0.data_ptr(), flags,
-        None if work is None else work.data_ptr(), size, _current(device)), "sla_recur_adjoint")
-    return (da if want_da else None), (db if want_db else None), dh0
+    if stream is not None:
+        with _on(stream, h):
+            return _load().recur_adjoint(a, h, dh, b, h0, seq_off, dh_last, gate, want_da, want_db, da, db)
+    return (_native or _load()).recur_adjoint(a, h, dh, b, h0, seq_off, dh_last, gate, want_da, want_db, da, db)
 
 
-@_placed
 def sla_recur_step(a: torch.Tensor, b: torch.Tensor, state: torch.Tensor, index: Optional[torch.Tensor] = None, *,
-                   gate: str = "value", out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                   gate: str = "value", out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """One token for each row of a serving batch: state[index[r]] = a_r state[index[r]] + w_r b_r in
     place; returns the new states' rows in b's type.  a, b: [rows, channels]; state: [slots,
     channels] float32 (float64); index: int32 [rows], distinct (None: row r has slot r).  Rows whose
     index is outside the pool are padding: no state changes, and they come back as zeros (with
     `out` given, as they were)."""
-    code, g = _code(b), _gate(gate)
-    if b.dim() != 2:
-        raise ValueError("rows must be [rows, channels]")
-    rows, channels = b.shape
-    lda, ldb, device = _rows(a, b, "a"), _rows(b, b, "b"), b.device
-    if (state.dim() != 2 or state.shape[1] != channels or state.dtype != _wide(b.dtype) or state.device != device):
-        raise ValueError(f"state must be [slots, {channels}] {_wide(b.dtype)} on {device}, got "
-                         f"{tuple(state.shape)} {state.dtype} on {state.device}")
-    lds = _rows(state, state, "state", out=True)
-    if index is None and state.shape[0] < rows:
-        raise ValueError("without index every row needs a slot")
-    flags = 0
-    if out is None:
-        out, ldh, flags = torch.empty((rows, channels), dtype=b.dtype, device=device), channels, _lib.SLA_FILL_REST
-    else:
-        ldh = _rows(out, b, "out", out=True)
-    _check(_lib.load().sla_recur_step(
-        code, g, rows, channels, state.shape[0], a.data_ptr(), lda, b.data_ptr(), ldb, state.data_ptr(), lds,
-        _plain(index, (rows,), torch.int32, device, "index"), out.data_ptr(), ldh, flags, _current(device)),
-        "sla_recur_step")
-    return out
+    if stream is not None:
+        with _on(stream, b):
+            return _load().recur_step(a, b, state, index, gate, out)
+    return (_native or _load()).recur_step(a, b, state, index, gate, out)
 
 
 class _Recurrence(torch.autograd.Function):
@@ -338,140 +180,62 @@ class Route:
         return self.entry.shape[0]
 
 
-def _check_route(r: Route, device: torch.device):
-    tokens, top_k = r.slot.shape
-    experts = r.counts.shape[0]
-    _plain(r.slot, (tokens, top_k), torch.int32, device, "route.slot")
-    _plain(r.offsets, (experts + 1,), torch.int32, device, "route.offsets")
-    _plain(r.counts, (experts,), torch.int32, device, "route.counts")
-    return tokens, top_k, experts, r.entry.shape[0]
-
-
-def _side(t: torch.Tensor, rows: int, name: str) -> int:
-    """Checks [rows, channels] rows; their row stride."""
-    if t.dim() != 2 or t.shape[0] != rows:
-        raise ValueError(f"{name} must have {rows} rows, got {tuple(t.shape)}")
-    return _rows(t, t, name)
-
-
-@_placed
-def sla_route_sort(expert: torch.Tensor, n_experts: int, *, align: int = 1, n_slots: Optional[int] = None) -> Route:
+def sla_route_sort(expert: torch.Tensor, n_experts: int, *, align: int = 1, n_slots: Optional[int] = None,
+                   stream=None) -> Route:
     """The plan that sorts tokens by expert.  expert: [tokens, top_k] (or [tokens]) int32 or int64 ids;
     ids outside [0, n_experts) are dropped.  Within an expert the order is that of the tokens (and
     choices).  Every expert's slots are padded to a multiple of `align` (a product's tile).
     n_slots: slots to provide (default, and least: tokens * top_k + n_experts * (align - 1))."""
-    if expert.dtype not in (torch.int32, torch.int64) or expert.dim() not in (1, 2) or not expert.is_contiguous():
-        raise ValueError("expert must be a contiguous [tokens, top_k] or [tokens] tensor of int32 or int64")
-    device = expert.device
-    tokens, top_k = (expert.shape[0], 1) if expert.dim() == 1 else expert.shape
-    if n_slots is None:
-        n_slots = tokens * top_k + n_experts * (align - 1)
-    if n_experts < 1 or align < 1 or top_k < 1 or n_slots < 0 or n_slots >= 2 ** 31:
-        raise ValueError("n_experts, align and top_k must be at least 1, and n_slots within [0, 2^31)")
-    # one allocation for the plan's four arrays, each on a 16-byte boundary
-    up = lambda n: (n + 3) // 4 * 4  # noqa: E731
-    o1 = up(n_experts + 1)
-    o2 = o1 + up(n_experts)
-    o3 = o2 + up(n_slots)
-    buf = torch.empty(o3 + tokens * top_k, dtype=torch.int32, device=device)
-    route = Route(buf[:n_experts + 1], buf[o1:o1 + n_experts], buf[o2:o2 + n_slots], buf[o3:].view(tokens, top_k))
-    size = _route_work(tokens, top_k, n_experts)
-    work = _scratch(size, device)
-    base = buf.data_ptr()
-    _check(_lib.load().sla_route_sort(
-        tokens, top_k, n_experts, align, expert.data_ptr(), expert.element_size(), n_slots, base, base + 4 * o1,
-        base + 4 * o2, base + 4 * o3, None if work is None else work.data_ptr(), size, _current(device)),
-        "sla_route_sort")
-    return route
+    if stream is not None:
+        with _on(stream, expert):
+            return Route(*_load().route_sort(expert, n_experts, align, n_slots))
+    return Route(*(_native or _load()).route_sort(expert, n_experts, align, n_slots))
 
 
-@_placed
+def _to_slots(x, route, weight, ys, out, stream):
+    if stream is not None:
+        with _on(stream, x):
+            return _to_slots(x, route, weight, ys, out, None)
+    return (_native or _load()).route_to_slots(x, route.offsets, route.counts, route.entry, route.slot, weight, ys, out)
+
+
+def _to_tokens(ys, route, weight, x, out, stream):
+    if stream is not None:
+        with _on(stream, ys):
+            return _to_tokens(ys, route, weight, x, out, None)
+    return (_native or _load()).route_to_tokens(ys, route.offsets, route.counts, route.entry, route.slot, weight, x, out)
+
+
 def sla_route_dispatch(x: torch.Tensor, route: Route, weight: Optional[torch.Tensor] = None, *,
-                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """xs = R^T x: every slot gets its token's row (times its weight), padding slots zeros.  x:
     [tokens, channels]; weight: [tokens, top_k] float32 (float64) or None for 1.  Slots behind the
     last expert's come back as zeros, or, with `out` given, as they were."""
-    return _to_slots(x, route, weight, None, out, False)[0]
+    return _to_slots(x, route, weight, None, out, stream)[0]
 
 
-@_placed
 def sla_route_combine_adjoint(dy: torch.Tensor, route: Route, ys: Optional[torch.Tensor] = None,
-                              weight: Optional[torch.Tensor] = None, *, out: Optional[torch.Tensor] = None):
+                              weight: Optional[torch.Tensor] = None, *, out: Optional[torch.Tensor] = None,
+                              stream=None):
     """Adjoint of sla_route_combine: (dL/dys = R^T dy, dL/dweight = dy . ys on R's pattern); the
     latter with ys given, else None.  Dropped entries have weight gradient 0."""
-    return _to_slots(dy, route, weight, ys, out, ys is not None)
+    return _to_slots(dy, route, weight, ys, out, stream)
 
 
-def _to_slots(x, route, weight, ys, out, want_dw):
-    code, device = _code(x), x.device
-    tokens, top_k, experts, slots = _check_route(route, device)
-    ldx, channels, wide = _side(x, tokens, "rows"), x.shape[1], _wide(x.dtype)
-    pw = _plain(weight, (tokens, top_k), wide, device, "weight")
-    flags = 0
-    if out is None:
-        out, ldo, flags = torch.empty((slots, channels), dtype=x.dtype, device=device), channels, _lib.SLA_FILL_REST
-    else:
-        if out.shape != (slots, channels) or out.dtype != x.dtype or out.device != device:
-            raise ValueError(f"out must be {(slots, channels)} {x.dtype} on {device}")
-        ldo = _rows(out, out, "out", out=True)
-    if not want_dw:
-        _check(_lib.load().sla_route_dispatch(
-            code, tokens, top_k, experts, slots, channels, x.data_ptr(), ldx, route.offsets.data_ptr(),
-            route.counts.data_ptr(), route.slot.data_ptr(), pw, out.data_ptr(), ldo, flags, _current(device)),
-            "sla_route_dispatch")
-        return out, None
-    if ys.shape != (slots, channels) or ys.dtype != x.dtype or ys.device != device:
-        raise ValueError(f"ys must be {(slots, channels)} {x.dtype} on {device}")
-    ldys = _rows(ys, ys, "ys")
-    dw = torch.empty((tokens, top_k), dtype=wide, device=device)
-    _check(_lib.load().sla_route_combine_adjoint(
-        code, tokens, top_k, experts, slots, channels, x.data_ptr(), ldx, route.offsets.data_ptr(),
-        route.counts.data_ptr(), route.slot.data_ptr(), pw, ys.data_ptr(), ldys, out.data_ptr(), ldo, dw.data_ptr(),
-        flags, _current(device)), "sla_route_combine_adjoint")
-    return out, dw
-
-
-@_placed
 def sla_route_combine(ys: torch.Tensor, route: Route, weight: Optional[torch.Tensor] = None, *,
-                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y = R ys: every token's sum over its slots, times their weights ([tokens, top_k] float32 or
     float64; None: 1), in the order of the choices; a token without slots gets zeros.
     ys: [slots, channels]; rows of slots without an entry are not read."""
-    return _to_tokens(ys, route, weight, None, out)[0]
+    return _to_tokens(ys, route, weight, None, out, stream)[0]
 
 
-@_placed
 def sla_route_dispatch_adjoint(dxs: torch.Tensor, route: Route, x: Optional[torch.Tensor] = None,
-                               weight: Optional[torch.Tensor] = None, *, out: Optional[torch.Tensor] = None):
+                               weight: Optional[torch.Tensor] = None, *, out: Optional[torch.Tensor] = None,
+                               stream=None):
     """Adjoint of sla_route_dispatch: (dL/dx = R dxs, dL/dweight = x . dxs on R's pattern); the
     latter with x given, else None.  Dropped entries have weight gradient 0."""
-    return _to_tokens(dxs, route, weight, x, out)
-
-
-def _to_tokens(ys, route, weight, x, out):
-    code, device = _code(ys), ys.device
-    tokens, top_k, _, slots = _check_route(route, device)
-    ldys, channels, wide = _side(ys, slots, "rows"), ys.shape[1], _wide(ys.dtype)
-    pw = _plain(weight, (tokens, top_k), wide, device, "weight")
-    if out is None:
-        out, ldo = torch.empty((tokens, channels), dtype=ys.dtype, device=device), channels
-    else:
-        if out.shape != (tokens, channels) or out.dtype != ys.dtype or out.device != device:
-            raise ValueError(f"out must be {(tokens, channels)} {ys.dtype} on {device}")
-        ldo = _rows(out, out, "out", out=True)
-    if x is None:
-        _check(_lib.load().sla_route_combine(
-            code, tokens, top_k, slots, channels, ys.data_ptr(), ldys, route.slot.data_ptr(), pw, out.data_ptr(), ldo,
-            _current(device)), "sla_route_combine")
-        return out, None
-    if x.dtype != ys.dtype or x.device != device or x.shape != (tokens, channels):
-        raise ValueError(f"x must be {(tokens, channels)} {ys.dtype} on {device}")
-    ldx = _rows(x, x, "x")
-    dw = torch.empty((tokens, top_k), dtype=wide, device=device)
-    _check(_lib.load().sla_route_dispatch_adjoint(
-        code, tokens, top_k, slots, channels, ys.data_ptr(), ldys, route.slot.data_ptr(), pw, x.data_ptr(), ldx,
-        out.data_ptr(), ldo, dw.data_ptr(), _current(device)), "sla_route_dispatch_adjoint")
-    return out, dw
+    return _to_tokens(dxs, route, weight, x, out, stream)
 
 
 class _Dispatch(torch.autograd.Function):

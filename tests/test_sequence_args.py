@@ -144,22 +144,34 @@ def test_adjoints_of_routing_refuse(lib):
 
 
 # ------------------------------------------------------------------------- the binding's checks
+# Shapes, types and strides are looked at before the device, so host tensors reach every refusal.
 
-def test_cpu_tensors_are_refused():
-    x = torch.zeros(4, 8)
-    off = torch.tensor([0, 4], dtype=torch.int32)
-    route = sla.Route(off, off[:1], off, torch.zeros(4, 1, dtype=torch.int32))
+@pytest.fixture(scope="module")
+def native(lib):
+    return sequence._load()
+
+
+def plan(tokens=4, top_k=1, experts=1, slots=4):
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    return sla.Route(z(experts + 1), z(experts), z(slots), z(tokens, top_k))
+
+
+def test_cpu_tensors_are_refused(native):
+    x, s = torch.zeros(4, 8), torch.zeros(1, 8)
+    ids = torch.zeros(4, dtype=torch.int32)
+    route = plan()
     for call in (lambda: sla.sla_recur_solve(x, x), lambda: sla.recurrence(x, x), lambda: sla.sla_recur_adjoint(x, x, x),
-                 lambda: sla.sla_recur_step(x, x, x), lambda: sla.sla_route_sort(off, 3),
+                 lambda: sla.sla_recur_step(x, x, x), lambda: sla.sla_route_sort(ids, 3),
                  lambda: sla.sla_route_dispatch(x, route), lambda: sla.sla_route_combine(x, route),
                  lambda: sla.route_dispatch(x, route), lambda: sla.route_combine(x, route),
-                 lambda: sla.sla_recur_solve(a=x, b=x), lambda: sla.sla_recur_solve([1.0], [2.0])):
+                 lambda: sla.sla_recur_solve(a=x, b=x, h0=s), lambda: sla.sla_recur_solve([1.0], [2.0]),
+                 lambda: sla.sla_recur_solve(x, None), lambda: sla.sla_recur_solve(x, x, stream=0)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
 
 
-def test_row_strides():
-    s = sequence._stride
+def test_row_strides(native):
+    s = native.stride_of
     x = torch.zeros(6, 8)
     assert s(x) == 8 and s(x[:, :5]) == 8 and s(x[::2]) == 16
     assert s(x[:1].expand(6, 8)) == 0                      # one row for all
@@ -175,29 +187,71 @@ def test_row_strides():
     assert s(sequence._walkable(y.transpose(0, 1))) == 8
 
 
-def test_binding_refuses():
+def test_recurrence_refuses(native):
     x = torch.zeros(4, 8)
-    with pytest.raises(ValueError, match="overlap"):
-        sequence._rows(x[:1].expand(4, 8), x, "out", out=True)
-    with pytest.raises(ValueError, match="stride"):
-        sequence._rows(x.t(), x.t(), "a")
-    with pytest.raises(ValueError, match="must be"):
-        sequence._rows(x.double(), x, "a")
-    with pytest.raises(ValueError, match="must be"):
-        sequence._rows(x[:3], x, "a")
-    with pytest.raises(ValueError, match="contiguous"):
-        sequence._plain(x.t(), (8, 4), torch.float32, x.device, "h0")
-    with pytest.raises(ValueError, match="must be"):
-        sequence._plain(x, (8, 4), torch.float32, x.device, "h0")
-    with pytest.raises(ValueError, match="rows must be"):
-        sequence._code(x.to(torch.int32))
-    with pytest.raises(ValueError, match="gate"):
-        sequence._gate("tanh")
     off = torch.tensor([0, 4], dtype=torch.int32)
-    with pytest.raises(ValueError, match="packed"):
-        sequence._sequences(x[None], off)
+    solve, adjoint, step = sla.sla_recur_solve, sla.sla_recur_adjoint, sla.sla_recur_step
+    for call, words in [
+            (lambda: solve(x, x, out=x[:1].expand(4, 8)), "overlap"),
+            (lambda: solve(x.t(), x.t()), "stride"),
+            (lambda: solve(x.double(), x), "a must be"),
+            (lambda: solve(x[:3], x), "a must be"),
+            (lambda: solve(x, x, out=x.bfloat16()), "out must be"),
+            (lambda: solve(x, x, torch.zeros(8, 1).t()[:, ::2], off), "h0 must be"),
+            (lambda: solve(x, x, torch.zeros(2, 8), off), "h0 must be"),
+            (lambda: solve(x, x, torch.zeros(1, 8).double(), off), "h0 must be"),
+            (lambda: solve(x[:, :1], x[:, :1], torch.zeros(2, 2)[:, :1], torch.zeros(3, dtype=torch.int32)), "contiguous"),
+            (lambda: solve(x, x, h_last=torch.zeros(2, 8)), "h_last must be"),
+            (lambda: solve(x.int(), x.int()), "rows must be"),
+            (lambda: solve(x, x, gate="tanh"), "gate"),
+            (lambda: solve(x, x, gate=None), "gate"),
+            (lambda: solve(x[None], x[None], None, off), "packed"),
+            (lambda: solve(x[0], x[0]), "rows must be"),
+            (lambda: adjoint(x, x, x, gate="sigmoid"), "needs b"),
+            (lambda: adjoint(x, x, x, da=x.clone()), "both"),
+            (lambda: adjoint(x, x, x[:2]), "dh must be"),
+            (lambda: adjoint(x, x, x, dh_last=torch.zeros(3, 8)), "dh_last must be"),
+            (lambda: adjoint(x, x, x, da=x[:1].expand(4, 8), db=x.clone()), "overlap"),
+            (lambda: adjoint(x, x, x, b=x[:, ::2], gate="sigmoid"), "b must be"),
+            (lambda: step(x, x, x[:3]), "slot"),
+            (lambda: step(x, x, x.bfloat16()), "state must be"),
+            (lambda: step(x, x, x[:1].expand(4, 8)), "overlap"),
+            (lambda: step(x, x, x, torch.arange(4)), "index must be"),
+            (lambda: step(x, x, x, torch.zeros(3, dtype=torch.int32)), "index must be"),
+            (lambda: step(x[None], x[None], x), "rows must be")]:
+        with pytest.raises(ValueError, match=words):
+            call()
     for bad in (off.long(), off[:0], off[None], torch.zeros(6, dtype=torch.int32)[::2]):
         with pytest.raises(ValueError, match="seq_off"):
-            sequence._sequences(x, bad)
-    with pytest.raises(ValueError, match="rows must be"):
-        sequence._sequences(x[0], None)
+            solve(x, x, None, bad)
+
+
+def test_routing_refuses(native):
+    x, w = torch.zeros(4, 8), torch.zeros(4, 1)
+    ids = torch.zeros(4, 2, dtype=torch.int64)
+    r = plan()
+    for call, words in [
+            (lambda: sla.sla_route_sort(ids.float(), 3), "expert must be"),
+            (lambda: sla.sla_route_sort(ids[:, :1], 3), "expert must be"),
+            (lambda: sla.sla_route_sort(ids[None], 3), "expert must be"),
+            (lambda: sla.sla_route_sort(ids, 0), "at least 1"),
+            (lambda: sla.sla_route_sort(ids, 3, align=0), "at least 1"),
+            (lambda: sla.sla_route_sort(ids[:, :0].contiguous(), 3), "at least 1"),
+            (lambda: sla.sla_route_sort(ids, 3, align=2 ** 30), "n_slots"),
+            (lambda: sla.sla_route_sort(ids, 3, n_slots=-1), "n_slots"),
+            (lambda: sla.sla_route_sort(ids, 2.5), "whole"),
+            (lambda: sla.sla_route_dispatch(x[:3], r), "rows must be"),
+            (lambda: sla.sla_route_dispatch(x.int(), r), "rows must be"),
+            (lambda: sla.sla_route_dispatch(x.t(), plan(tokens=8)), "stride"),
+            (lambda: sla.sla_route_dispatch(x, r, w.double()), "weight must be"),
+            (lambda: sla.sla_route_dispatch(x, r, w[:, 0]), "weight must be"),
+            (lambda: sla.sla_route_dispatch(x, r, out=x[:3]), "out must be"),
+            (lambda: sla.sla_route_dispatch(x, r, out=x[:1].expand(4, 8)), "overlap"),
+            (lambda: sla.sla_route_dispatch(x, sla.Route(r.offsets, r.counts, r.entry, r.slot.long())), "route.slot"),
+            (lambda: sla.sla_route_dispatch(x, sla.Route(r.counts, r.counts, r.entry, r.slot)), "route.offsets"),
+            (lambda: sla.sla_route_combine(x, plan(slots=5)), "rows must be"),
+            (lambda: sla.sla_route_combine(x, r, out=x.double()), "out must be"),
+            (lambda: sla.sla_route_dispatch_adjoint(x, r, x[:, :4]), "x must be"),
+            (lambda: sla.sla_route_combine_adjoint(x, r, x.bfloat16()), "ys must be")]:
+        with pytest.raises(ValueError, match=words):
+            call()
