@@ -386,7 +386,8 @@ struct TilePlan {
     int tile;                  // -1: no more tiles
     int chunk, cb;
     int lo, hi;                // positions of the tile inside [first, last) row of all sequences
-    int seg;                   // borders or rows outside the sequences in the tile: use the flags
+    int first;                 // the sequence that the scan enters at the tile's first position, or -1
+    int seg;                   // other borders, or rows outside the sequences, in the tile: use the flags
 };
 
 template <typename S, int GATE, bool REV>
@@ -626,7 +627,7 @@ struct Recur {
             if constexpr (!REV) {
                 if constexpr (GATE == SLA_GATE_SIGMOID)
                     vmul(x, w, x);
-                if (first || (SEG && s >= 0 && !g.enter))
+                if (first)
 #pragma unroll
                     for (int v = 0; v < V; ++v)
                         mh[v] = x[v];
@@ -767,12 +768,7 @@ struct Recur {
             if constexpr (!REV) {
                 if constexpr (GATE == SLA_GATE_SIGMOID)
                     vmul(y, w, y);
-                if (SEG && s >= 0 && !g.enter)
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        x[v] = y[v];
-                else
-                    vfma(x, a, x, y);
+                vfma(x, a, x, y);
                 store(0, i, t, c0, st, sx, x);
             } else {
                 A hb[V], lam[V];
@@ -893,12 +889,19 @@ struct Recur {
     // products leave the range.
     __device__ __forceinline__ void front_states(int buf, int place, A x)
     {
-#pragma unroll 4
-        for (int r = 0; r < P::NR; ++r) {
-            const A a = sm.mapA[buf][r][place], h = sm.mapH[buf][r][place];
-            sm.mapA[buf][r][place] = const_mark<A>();
-            sm.mapH[buf][r][place] = x;
-            x = apply(a, x, h);
+        for (int r0 = 0; r0 < P::NR; r0 += 4) {
+            A a[4], h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                a[k] = sm.mapA[buf][r0 + k][place];
+                h[k] = sm.mapH[buf][r0 + k][place];
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                sm.mapA[buf][r0 + k][place] = const_mark<A>();
+                sm.mapH[buf][r0 + k][place] = x;
+                x = apply(a[k], x, h[k]);
+            }
         }
     }
     // whether the runs' maps may be composed in their own type: no borders, everything finite
@@ -932,28 +935,33 @@ struct Recur {
         sm.tileH[buf][place] = th;
         if (pl.chunk + 1 < g.n_chunks && ch < g.n_chan) {
             const int64_t cell = (int64_t)pl.chunk * g.n_chan + ch;
-            if (pl.chunk == 0 || Wd::fixed(pa))
+            if (Wd::fixed(pa))
                 st_word((typename Wd::Inc *)g.inc + cell, Wd::inc_bits(th));
-            else
+            else if (enters(pl))
                 Wd::put(g.agg + cell * Wd::N, pa, th);
         }
     }
 
-    // whether the state before the tile is needed: not where a border (or a row outside) is at its first position
-    __device__ __forceinline__ bool enters(const TilePlan &pl, int slot) const
+    // whether the tile's own state depends on the chunks before it: not where a border (or a row outside) is at its
+    // first position
+    __device__ __forceinline__ bool enters(const TilePlan &pl) const
     {
-        return pl.chunk > 0 && !(pl.seg && (pl.lo > 0 || pl.hi == 0 || sm.begin[slot][0] >= 0));
+        return pl.chunk > 0 && pl.first < 0 && pl.lo == 0 && pl.hi > 0;
     }
     // one channel of a tile: the state that enters it
-    __device__ __forceinline__ A find_state(const TilePlan &pl, int slot, int place) const
+    __device__ __forceinline__ A find_state(const TilePlan &pl, int place) const
     {
         const int64_t ch = (int64_t)pl.cb * P::W + chan_at(place);
-        if (ch >= g.n_chan || !enters(pl, slot))
+        if (ch >= g.n_chan)
+            return A(0);
+        if (pl.first >= 0)
+            return enter_of(pl.first, ch);
+        if (!enters(pl))
             return A(0);
         return state_before<A>(pl.chunk, g.n_chan, ch, g.n_cb * 4 < (int)gridDim.x, g.agg, (const typename Words<A>::Inc *)g.inc);
     }
     // its leaving state, published, and where the maps do not compose the runs' states
-    __device__ __forceinline__ void hand_over(const TilePlan &pl, int slot, int buf, int place, A x)
+    __device__ __forceinline__ void hand_over(const TilePlan &pl, int buf, int place, A x)
     {
         using Wd = Words<A>;
         const int64_t ch = (int64_t)pl.cb * P::W + chan_at(place);
@@ -962,7 +970,7 @@ struct Recur {
         sm.enter[buf][place] = x;
         if (ch >= g.n_chan)
             return;
-        if (pl.chunk + 1 < g.n_chunks && !Wd::fixed(pa) && enters(pl, slot))
+        if (pl.chunk + 1 < g.n_chunks && !Wd::fixed(pa))
             st_word((typename Wd::Inc *)g.inc + (int64_t)pl.chunk * g.n_chan + ch, Wd::inc_bits(Wd::apply(pa, x, th)));
         if (!plain(pl, pa, th))
             front_states(buf, place, x);
@@ -974,7 +982,9 @@ struct Recur {
         TilePlan pl;
         const int64_t tiles = (int64_t)g.n_chunks * g.n_cb;
         int64_t tile;
-        if (g.ticket) {
+        if (k > 0 && tiles <= gridDim.x)                   // a tile a block
+            tile = tiles;
+        else if (g.ticket) {
             unsigned v = 0;
             if (lane == 0)
                 v = atomicAdd(g.ticket, 1u) + 1u;          // the counter starts at all bits set
@@ -994,48 +1004,69 @@ struct Recur {
         const int64_t pos1 = min(n, pos0 + C);
         // the tile's rows in row order
         const int64_t r0 = REV ? n - pos1 : pos0, r1 = REV ? n - pos0 : pos1;
-        const int64_t lo = g.q.n_seq > 0 ? g.q.at(0) : 0, hi = g.q.n_seq > 0 ? max(lo, g.q.at(g.q.n_seq)) : 0;
+        // the offsets of up to 31 sequences in one look, or the first one that ends behind r0 by 32 probes at a time
+        const int32_t n_seq = g.q.n_seq;
+        const bool few = n_seq < 32;
+        int64_t off = few && lane <= n_seq && n_seq > 0 ? g.q.at(lane) : INT64_MAX;
+        int64_t lo, hi, s0 = 0;
+        if (few) {
+            lo = n_seq > 0 ? __shfl_sync(0xffffffffu, off, 0) : 0;
+            hi = n_seq > 0 ? __shfl_sync(0xffffffffu, off, n_seq) : 0;
+        } else {
+            lo = g.q.at(0);
+            hi = g.q.at(n_seq);
+            int64_t s1 = n_seq;                            // it is in [s0, s1]
+            while (s1 - s0 > 32) {
+                const int64_t step = (s1 - s0 + 31) / 32;
+                const int64_t s = min(s0 + step * (lane + 1) - 1, s1 - 1);
+                const unsigned behind = __ballot_sync(0xffffffffu, g.q.at(s + 1) > r0);
+                const int64_t b0 = s0 + step * (behind ? __ffs(behind) - 1 : 31);
+                s1 = behind ? min(s1, b0 + step - 1) : s1;
+                s0 = behind ? min(b0, s1) : s1;
+            }
+        }
+        hi = max(lo, hi);
         const int64_t v0 = min(max(lo, r0), r1), v1 = max(v0, min(hi, r1));
         pl.lo = (int)(REV ? r1 - v1 : v0 - r0);
         pl.hi = (int)(REV ? r1 - v0 : v1 - r0);
-        // the first sequence that ends behind r0: of 32 probes at a time
-        int64_t s0 = 0, s1 = g.q.n_seq;                    // it is in [s0, s1]
-        while (s1 - s0 > 32) {
-            const int64_t step = (s1 - s0 + 31) / 32;
-            const int64_t s = min(s0 + step * (lane + 1) - 1, s1 - 1);
-            const unsigned behind = __ballot_sync(0xffffffffu, g.q.at(s + 1) > r0);
-            const int k0 = behind ? __ffs(behind) - 1 : 31;
-            const int64_t b0 = s0 + step * k0;
-            s1 = behind ? min(s1, b0 + step - 1) : s1;
-            s0 = min(b0, s1);
-            if (!behind)
-                s0 = s1;
-        }
         bool seg = pl.lo > 0 || pl.hi < C, cleared = false;
+        int first = -1;
         for (int64_t s = s0;; s += 32) {
             const int64_t mine = s + lane;
             int64_t b = INT64_MAX, e = -1;
-            if (mine < g.q.n_seq) {
+            if (few) {
+                const int64_t next = __shfl_down_sync(0xffffffffu, off, 1);
+                if (lane < n_seq) {
+                    b = off;
+                    e = next - 1;
+                }
+            } else if (mine < n_seq) {
                 b = g.q.at(mine);
                 e = g.q.at(mine + 1) - 1;                  // last row
             }
-            const bool full = e >= b && mine < g.q.n_seq;
+            const bool full = mine < n_seq && e >= b;
             const bool bin = full && b >= r0 && b < r1, ein = full && e >= r0 && e < r1;
-            const bool any = __any_sync(0xffffffffu, bin || ein);
+            // positions where the scan enters and leaves the sequence
+            const int pb = REV ? (int)(r1 - 1 - b) : (int)(b - r0), pe = REV ? (int)(r1 - 1 - e) : (int)(e - r0);
+            const int in = REV ? (ein ? pe : -1) : (bin ? pb : -1), leave = REV ? (bin ? pb : -1) : (ein ? pe : -1);
+            const unsigned at0 = __ballot_sync(0xffffffffu, in == 0);
+            if (at0)
+                first = (int)(s + __ffs(at0) - 1);
+            const bool any = __any_sync(0xffffffffu, in > 0 || leave >= 0);
             if ((any || seg) && !cleared) {
                 for (int p = lane; p < C; p += 32)
                     sm.begin[slot][p] = sm.finish[slot][p] = -1;
                 __syncwarp();
                 cleared = seg = true;
             }
-            if (bin)
-                (REV ? sm.finish : sm.begin)[slot][REV ? (int)(r1 - 1 - b) : (int)(b - r0)] = (int)mine;
-            if (ein)
-                (REV ? sm.begin : sm.finish)[slot][REV ? (int)(r1 - 1 - e) : (int)(e - r0)] = (int)mine;
-            const int64_t next = s + 32;
-            if (next >= g.q.n_seq || __all_sync(0xffffffffu, b >= r1))
+            if (in > 0)
+                sm.begin[slot][in] = (int)mine;
+            if (leave >= 0)
+                sm.finish[slot][leave] = (int)mine;
+            if (s + 32 >= n_seq || __all_sync(0xffffffffu, b >= r1))
                 break;
         }
+        pl.first = first;
         pl.seg = seg;
         if (lane == 0)
             sm.plan[slot] = pl;
@@ -1064,6 +1095,12 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
 
     if (r.tid < P::NC) {                                   // compute warps
         typename K::Kept now, next;
+        // while the first plan is made: empty sequences leave with what entered them
+        if (g.leave && (g.q.off || g.q.n_tokens == 0))
+            for (int64_t s = blockIdx.x; s < g.q.n_seq; s += gridDim.x)
+                if (g.q.at(s + 1) <= g.q.at(s))
+                    for (int64_t c = r.tid; c < g.n_chan; c += P::NC)
+                        g.leave[s * g.n_chan + c] = g.enter ? g.enter[s * g.n_chan + c] : A(0);
         bar_sync(BAR_FIRST, P::NT);                        // plan 0
         if constexpr (!K::BOX) {
             r.load(sm.plan[0], 0);
@@ -1107,12 +1144,6 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
         }
         if constexpr (!K::BOX)
             asm volatile("cp.async.wait_all;" ::: "memory");
-        // empty sequences leave with what entered them
-        if (g.leave)
-            for (int64_t s = blockIdx.x; s < g.q.n_seq; s += gridDim.x)
-                if (g.q.at(s + 1) <= g.q.at(s))
-                    for (int64_t c = r.tid; c < g.n_chan; c += P::NC)
-                        g.leave[s * g.n_chan + c] = g.enter ? g.enter[s * g.n_chan + c] : A(0);
     } else if (r.tid < P::NC + P::NK) {                    // map warps
         bar_sync(BAR_FIRST, P::NT);
         for (int slot = 0, odd = 0;; slot = up(slot, NP), odd ^= 1) {
@@ -1138,11 +1169,11 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
                 break;
             A x = A(0);
             if (place < P::W)
-                x = r.find_state(pl, slot, place);
+                x = r.find_state(pl, place);
             __syncwarp();
             bar_sync(BAR_TILE + odd, TILE);
             if (place < P::W)
-                r.hand_over(pl, slot, odd, place, x);
+                r.hand_over(pl, odd, place, x);
             __syncwarp();
             bar_arrive(BAR_ENTER + odd, ENTER);
         }

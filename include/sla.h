@@ -367,7 +367,8 @@ SLA_API sla_status sla_pcg_solve_batched_noalloc(const sla_csr *A, const sla_pre
  *   - Packed sequences: sequence s owns rows [d_seq_off[s], d_seq_off[s+1]) of the packed rows
  *     (device int32, n_seq + 1 entries, ascending, within [0, n_tokens]; empty sequences
  *     allowed).  NULL: n_seq sequences of n_tokens / n_seq rows each.  Rows outside every
- *     sequence are not read; they are left as they were, or set to zero with SLA_FILL_REST.
+ *     sequence do not count (whatever they hold); outputs leave them as they were, or set them to
+ *     zero with SLA_FILL_REST.
  *   - None of the calls allocates, synchronises or keeps anything: scratch memory is the
  *     caller's d_work (16-byte aligned; its contents before and after are unspecified).  Calls
  *     that may run at the same time, replays of captured graphs among them, need a d_work
@@ -388,7 +389,7 @@ typedef enum {
 SLA_API size_t sla_recur_workspace_bytes(int32_t dtype, int64_t n_tokens, int64_t n_chan);
 
 /* h_t = a_t h_{t-1} + w_t b_t over every sequence, from d_h0 (n_seq x n_chan, fp32 or fp64;
- * NULL: zero state, and then the coefficient of a sequence's first row is not used).  d_h gets
+ * NULL: zero states).  d_h gets
  * the rows; d_h_last (n_seq x n_chan, fp32/fp64, may be NULL) the unrounded last states (an empty
  * sequence's is its first one).  flags: 0 or SLA_FILL_REST. */
 SLA_API sla_status sla_recur_solve(int32_t dtype, int32_t gate, int64_t n_tokens, int64_t n_chan,
