@@ -8,28 +8,58 @@ namespace {
 
 constexpr int RT = 128;
 
-template <typename S, int GATE>
+// One row for each sequence of a serving batch.  A thread takes V channels of a row: 16 bytes of a, b and h where
+// everything is aligned to it, one value otherwise.  Bound by memory: 3 values and a state in and out a channel.
+template <typename S, int GATE, int V>
 __global__ void __launch_bounds__(RT)
     k_recur_step(int64_t n_rows, int64_t n_chan, int64_t n_slots, const S *a, int64_t lda, const S *b, int64_t ldb,
                  typename RowType<S>::A *state, int64_t lds, const int32_t *index, S *h, int64_t ldh, int fill)
 {
     using R = RowType<S>;
     using A = typename R::A;
-    const int64_t c = (int64_t)blockIdx.x * RT + threadIdx.x;
+    const int64_t c = ((int64_t)blockIdx.x * RT + threadIdx.x) * V;
     if (c >= n_chan)
         return;
     for (int64_t r = blockIdx.y; r < n_rows; r += gridDim.y) {
         const int64_t i = index ? index[r] : r;
-        if (i < 0 || i >= n_slots) {
-            if (fill)
-                h[r * ldh + c] = S(0.0f);
+        const bool live = i >= 0 && i < n_slots;
+        if (!live && !fill)
             continue;
+        constexpr int N = V > 1 ? V : 2;                   // arithmetic goes in pairs
+        A x[N] = {};
+        if (live) {
+            A z[N] = {}, u[N] = {}, w[N], v[N] = {};
+            A *st = state + i * lds + c;
+            if constexpr (V > 1) {
+                const uint4 ra = *reinterpret_cast<const uint4 *>(a + r * lda + c), rb = *reinterpret_cast<const uint4 *>(b + r * ldb + c);
+                uint4 rs[V * sizeof(A) / 16];
+#pragma unroll
+                for (int k = 0; k < (int)(V * sizeof(A) / 16); ++k)
+                    rs[k] = reinterpret_cast<const uint4 *>(st)[k];
+                unpack16(ra, z, S());
+                unpack16(rb, u, S());
+                memcpy(v, rs, sizeof(rs));
+            } else {
+                z[0] = R::up(a[r * lda + c]);
+                u[0] = R::up(b[r * ldb + c]);
+                v[0] = st[0];
+            }
+            gates_of<GATE, sizeof(S) == 2>(z, z, w);
+            vmul(u, w, u);
+            vfma(x, z, v, u);
+            if constexpr (V > 1) {
+                uint4 rs[V * sizeof(A) / 16];
+                memcpy(rs, x, sizeof(rs));
+#pragma unroll
+                for (int k = 0; k < (int)(V * sizeof(A) / 16); ++k)
+                    reinterpret_cast<uint4 *>(st)[k] = rs[k];
+            } else
+                st[0] = x[0];
         }
-        A z[2] = {R::up(a[r * lda + c]), A(0)}, ca[2], w[2];
-        gates_of<GATE, sizeof(S) == 2>(z, ca, w);
-        const A v = fma_of(ca[0], state[i * lds + c], mul_of(w[0], R::up(b[r * ldb + c])));
-        state[i * lds + c] = v;
-        h[r * ldh + c] = R::down(v);
+        if constexpr (V > 1)
+            *reinterpret_cast<uint4 *>(h + r * ldh + c) = pack16(x, S());
+        else
+            h[r * ldh + c] = R::down(x[0]);
     }
 }
 
@@ -238,9 +268,19 @@ sla_status sla_recur_step(int32_t dtype, int32_t gate, int64_t n_rows, int64_t n
         using S = decltype(tag);
         using A = typename RowType<S>::A;
         return with_gate(gate, [&](auto g) {
-            k_recur_step<S, decltype(g)::value><<<grid_of(n_chan, n_rows), RT, 0, s>>>(
-                n_rows, n_chan, n_slots, (const S *)d_a, lda, (const S *)d_b, ldb, (A *)d_state, ldstate, d_index,
-                (S *)d_h, ldh, (flags & SLA_FILL_REST) != 0);
+            constexpr int GATE = decltype(g)::value, V = 16 / (int)sizeof(S);
+            const uintptr_t bits = (uintptr_t)d_a | (uintptr_t)d_b | (uintptr_t)d_h | (uintptr_t)d_state |
+                                   (uintptr_t)((lda | ldb | ldh | n_chan) * (int64_t)sizeof(S)) |
+                                   (uintptr_t)(ldstate * (int64_t)sizeof(A));
+            auto run = [&](auto kernel, int v) {
+                kernel<<<grid_of((n_chan + v - 1) / v, n_rows), RT, 0, s>>>(
+                    n_rows, n_chan, n_slots, (const S *)d_a, lda, (const S *)d_b, ldb, (A *)d_state, ldstate, d_index,
+                    (S *)d_h, ldh, (flags & SLA_FILL_REST) != 0);
+            };
+            if (bits % 16 == 0)
+                run(k_recur_step<S, GATE, V>, V);
+            else
+                run(k_recur_step<S, GATE, 1>, 1);
             SLA_CUDA_TRY(cudaGetLastError());
             return (sla_status)SLA_SUCCESS;
         });

@@ -70,8 +70,8 @@ __device__ __forceinline__ void padded_offsets(int n, int align, const int *cnt,
 }
 
 // offsets, counts and the -1 of slots without an entry, shared out over `parts` blocks
-__device__ __forceinline__ void write_plan(int n_experts, int64_t n_slots, const int *cnt, const int *off, int part,
-                                           int parts, int32_t *offsets, int32_t *counts, int32_t *entry)
+__device__ __forceinline__ void write_plan(int n_experts, int align, int64_t n_slots, const int *cnt,
+                                           const int *off, int part, int parts, int32_t *offsets, int32_t *counts, int32_t *entry)
 {
     if (part == 0) {
         for (int e = threadIdx.x; e <= n_experts; e += blockDim.x)
@@ -79,10 +79,13 @@ __device__ __forceinline__ void write_plan(int n_experts, int64_t n_slots, const
         for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
             counts[e] = cnt[e];
     }
-    const int warps = parts * (blockDim.x >> 5), lane = threadIdx.x & 31;
-    for (int e = part * (blockDim.x >> 5) + (threadIdx.x >> 5); e < n_experts; e += warps)
-        for (int64_t p = (int64_t)off[e] + cnt[e] + lane; p < off[e + 1]; p += 32)
-            entry[p] = -1;
+    // a thread an expert where padding is short, a warp where it is long
+    const int lanes = align > 16 ? 32 : 1, lane = threadIdx.x & (lanes - 1);
+    const int64_t t = (int64_t)part * blockDim.x + threadIdx.x;
+    if (align > 1)
+        for (int64_t e = t / lanes; e < n_experts; e += (int64_t)parts * blockDim.x / lanes)
+            for (int64_t p = (int64_t)off[e] + cnt[e] + lane; p < off[e + 1]; p += lanes)
+                entry[p] = -1;
     for (int64_t p = off[n_experts] + (int64_t)part * blockDim.x + threadIdx.x; p < n_slots; p += (int64_t)parts * blockDim.x)
         entry[p] = -1;
 }
@@ -96,7 +99,7 @@ static inline size_t sort_smem(int n_experts, int warps)
 
 template <typename I, bool ALONE>
 __global__ void __launch_bounds__(ST)
-    k_route_rank(int64_t n, int64_t per_block, int n_experts, int align, const I *ids, int64_t n_slots, int32_t *offsets,
+    k_route_rank(int64_t n, int64_t per_block, int turns, int n_experts, int align, const I *ids, int64_t n_slots, int32_t *offsets,
                  int32_t *counts, int32_t *entry, int32_t *slot, int32_t *hist)
 {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -109,18 +112,20 @@ __global__ void __launch_bounds__(ST)
     const int64_t b0 = min(n, per_block * blockIdx.x), b1 = min(n, b0 + per_block);
     for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
         run[e] = sum[e] = 0;
-    for (int64_t tile = b0; tile < b1 || (ALONE && tile == b0); tile += (int64_t)warps * 32 * IT) {
-        const int64_t e0 = tile + (int64_t)warp * 32 * IT + lane;
+    for (int64_t tile = b0; tile < b1 || (ALONE && tile == b0); tile += (int64_t)warps * 32 * turns) {
+        const int64_t e0 = tile + (int64_t)warp * 32 * turns + lane;
         int x[IT], rank[IT];
 #pragma unroll
         for (int i = 0; i < IT; ++i)
-            x[i] = e0 + 32 * i < b1 ? expert_of(ids[e0 + 32 * i], n_experts) : -2;
+            x[i] = i < turns && e0 + 32 * i < b1 ? expert_of(ids[e0 + 32 * i], n_experts) : -2;
         for (size_t i = threadIdx.x; i < (cells + 7) / 8; i += blockDim.x)
             reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
         uint16_t *mine = cnt + (size_t)warp * n_experts;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
+            if (i >= turns)
+                break;
             const unsigned peers = __match_any_sync(0xffffffffu, x[i]);
             const int before = x[i] >= 0 ? mine[x[i]] : 0;
             rank[i] = before + __popc(peers & ((1u << lane) - 1));
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__(ST)
         __syncthreads();
     }
     if constexpr (ALONE)
-        write_plan(n_experts, n_slots, sum, off, 0, 1, offsets, counts, entry);
+        write_plan(n_experts, align, n_slots, sum, off, 0, 1, offsets, counts, entry);
     else
         for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
             hist[(size_t)blockIdx.x * n_experts + e] = sum[e];
@@ -214,7 +219,7 @@ __global__ void __launch_bounds__(ST)
             }
         }
     }
-    write_plan(n_experts, n_slots, cnt, off, blockIdx.x, gridDim.x, offsets, counts, entry);
+    write_plan(n_experts, align, n_slots, cnt, off, blockIdx.x, gridDim.x, offsets, counts, entry);
 }
 
 // Blocks of the two-launch sort: a tile each at least, at most 148, and histograms of 64 Ki numbers at most,
@@ -743,16 +748,17 @@ sla_status sla_route_sort(int64_t n_tokens, int32_t top_k, int32_t n_experts, in
     auto run = [&](auto ids) -> sla_status {
         using I = std::remove_const_t<std::remove_pointer_t<decltype(ids)>>;
         if (blocks == 1) {
-            const int w = (int)std::min<int64_t>(warps, std::max<int64_t>({1, (n + 32 * IT - 1) / (32 * IT),
-                                                                          ((int64_t)n_experts + 127) / 128}));
+            // few entries: a lane takes one, as long as there are warps
+            const int w = (int)std::min<int64_t>(warps, std::max<int64_t>({1, (n + 31) / 32, ((int64_t)n_experts + 31) / 32}));
+            const int turns = (int)std::max<int64_t>(1, (n + 32 * w - 1) / (32 * w));
             SLA_TRY(allow(k_route_rank<I, true>));
-            k_route_rank<I, true><<<1, 32 * w, smem, s>>>(n, n, n_experts, align, ids, n_slots, d_offsets, d_counts,
+            k_route_rank<I, true><<<1, 32 * w, smem, s>>>(n, n, turns, n_experts, align, ids, n_slots, d_offsets, d_counts,
                                                          d_entry, d_slot, nullptr);
         } else {
             const int64_t tile = (int64_t)warps * 32 * IT, per = ((n + blocks - 1) / blocks + tile - 1) / tile * tile;
             const unsigned grid = (unsigned)((n + per - 1) / per);
             SLA_TRY(allow(k_route_rank<I, false>));
-            k_route_rank<I, false><<<grid, 32 * warps, smem, s>>>(n, per, n_experts, align, ids, n_slots, d_offsets,
+            k_route_rank<I, false><<<grid, 32 * warps, smem, s>>>(n, per, IT, n_experts, align, ids, n_slots, d_offsets,
                                                                  d_counts, d_entry, d_slot, (int32_t *)d_work);
             const size_t smem2 = sizeof(int) * (3 * (size_t)n_experts + 1);
             SLA_TRY(allow(k_route_place<I>));
