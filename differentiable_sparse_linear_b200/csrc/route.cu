@@ -16,7 +16,7 @@ constexpr int MAX_EXPERTS = 4096;
 // ------------------------------------------------------------------ sort
 // A stable counting sort.  A block takes its run of entries in tiles; in a tile warp w owns 32 IT
 // consecutive entries and counts them by expert in cnt[w][.] as it goes: equal experts among 32 lanes are
-// ranked by lane (match), so an entry's rank within its warp and expert follows the order of the numbers.
+// ranked by lane (votes), so an entry's rank within its warp and expert follows the order of the numbers.
 // Prefix sums over the warps, the tiles and (k_route_place) the blocks turn ranks into slots.
 //
 // Up to one tile of entries (8192 at 256 experts) one block does all of it in one launch.  Above, blocks rank
@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(ST)
     int *sum = run + n_experts;                                             // ... up to this tile
     int *off = sum + n_experts;
     const int64_t b0 = min(n, per_block * blockIdx.x), b1 = min(n, b0 + per_block);
+    const int bits = 32 - __clz(n_experts);
     for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
         run[e] = sum[e] = 0;
     for (int64_t tile = b0; tile < b1 || (ALONE && tile == b0); tile += (int64_t)warps * 32 * turns) {
@@ -126,7 +127,13 @@ __global__ void __launch_bounds__(ST)
         for (int i = 0; i < IT; ++i) {
             if (i >= turns)
                 break;
-            const unsigned peers = __match_any_sync(0xffffffffu, x[i]);
+            // lanes of the same expert: a vote for each bit (dropped entries and lanes without one count as one more)
+            unsigned peers = 0xffffffffu;
+            const int key = x[i] < 0 ? n_experts : x[i];
+            for (int b = 0; b < bits; ++b) {
+                const unsigned set = __ballot_sync(0xffffffffu, key >> b & 1);
+                peers &= key >> b & 1 ? set : ~set;
+            }
             const int before = x[i] >= 0 ? mine[x[i]] : 0;
             rank[i] = before + __popc(peers & ((1u << lane) - 1));
             __syncwarp();
