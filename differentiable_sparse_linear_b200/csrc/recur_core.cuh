@@ -22,8 +22,8 @@
 //               stores;
 //   plan warp   the ticket of tile i + 3, the sequence borders in it, and its rows into shared memory by one tensor
 //               copy an input (backward, what only pass 2 reads: of tile i + 1).  Where rows are not aligned to
-//               16 bytes every compute thread copies its own values instead, by units of 4 bytes or one
-//               by one.
+//               16 bytes every compute warp copies its own rows instead, by units of 4 bytes (fp64: 8) or
+//               value by value.
 // So each input is read once and each gate evaluated once, and the wait on earlier chunks passes while the
 // compute warps are at another tile.  They meet once a tile, where they take over the entering states.
 //
@@ -144,6 +144,10 @@ __device__ __forceinline__ void box_in(void *dst, const CUtensorMap *map, int x,
                  "l"(map), "r"(x), "r"(y), "r"(smem_at(bar))
                  : "memory");
 }
+__device__ __forceinline__ void mbar_arrive(unsigned long long *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_at(bar)) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive_after_copies(unsigned long long *bar)
 {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_at(bar)) : "memory");
@@ -244,8 +248,6 @@ struct Words<float> {
         const unsigned f = mag < (897u << 20) ? 0u : (mag - (896u << 20)) << 3;
         return __fmaf_rn(__uint_as_float((a & 0x80000000u) | f), x, h);
     }
-    // within fp32's range
-    static __device__ __forceinline__ bool finite(unsigned a) { return (a & 0x7fffffffu) < ((1023u + 128u) << 20); }
     static __device__ __forceinline__ void put(unsigned long long *p, unsigned a, float h)
     {
         st_word(p, ((unsigned long long)a << 32) | __float_as_uint(h));
@@ -270,7 +272,6 @@ struct Words<double> {
         return x == x ? (unsigned long long)__double_as_longlong(x) : QUIET;
     }
     static __device__ __forceinline__ double pack(double a) { return a; }
-    static __device__ __forceinline__ bool finite(double a) { return isfinite(a); }
     static __device__ __forceinline__ double apply(double a, double x, double h) { return apply_wide(a, x, h); }
     static __device__ __forceinline__ void put(unsigned long long *p, double a, double h)
     {
@@ -388,6 +389,7 @@ struct TilePlan {
     int lo, hi;                // positions of the tile inside [first, last) row of all sequences
     int first;                 // the sequence that the scan enters at the tile's first position, or -1
     int seg;                   // other borders, or rows outside the sequences, in the tile: use the flags
+    int cut;                   // ... such that no state goes through the tile
 };
 
 template <typename S, int GATE, bool REV>
@@ -405,6 +407,7 @@ struct RecurSmem {
     typename Words<A>::Map tileA[P::NB][P::W];     // the tile's map as published
     A tileH[P::NB][P::W];
     A enter[P::NB][P::W];                          // the state that enters the tile
+    unsigned char fronts[P::NB][P::W];             // how the runs' maps are composed
     int begin[P::NP][P::C], finish[P::NP][P::C];   // sequence the scan enters / leaves at a position, or -1
     TilePlan plan[P::NP];
 };
@@ -426,8 +429,9 @@ struct Recur {
     const int p0;                                          // its first position
     bool lost = false;                                     // a load did not arrive
 
-    __device__ __forceinline__ Recur(const RecurArgs<S> &g_, Sm &sm_)
-        : g(g_), sm(sm_), tid(threadIdx.x), warp(tid >> 5), lane(tid & 31), l8(lane & 7),
+    // tid: among the compute threads
+    __device__ __forceinline__ Recur(const RecurArgs<S> &g_, Sm &sm_, int tid_)
+        : g(g_), sm(sm_), tid(tid_), warp(tid >> 5), lane(threadIdx.x & 31), l8(lane & 7),
           run(tid >> 3), p0(run * R)
     {
     }
@@ -497,33 +501,55 @@ struct Recur {
             box_in(dst, &g.map[k], x, y, bar);
         }
     }
-    // A thread starts the copies of its own values of a tile's rows of input K.
+    // A warp starts the copies of its 16 rows of input K of a tile, a row (or 128 bytes of two) an instruction.
     template <int K>
     __device__ __forceinline__ void copy_rows(const TilePlan &pl, int st)
     {
         if (!reads(K))
             return;
-        const int64_t c0 = (int64_t)pl.cb * P::W + l8 * V;
+        constexpr int LANES = P::W / U < 32 ? P::W / U : 32, ROWS = 32 / LANES, TURNS = P::W / U / LANES;
         constexpr int back = REV && K == 2;                // the state before the row
-        const int64_t t0 = row_of(pl, p0) - back, left = g.n_chan - c0;
-        const S *src = g.in[K] + t0 * g.ldin[K] + c0;
-        const int64_t step = REV ? -g.ldin[K] : g.ldin[K];
+        const int64_t c0 = (int64_t)pl.cb * P::W;
+        const int r = lane / LANES, u = lane % LANES * U, first = warp * 16 + r;
+        const int64_t t0 = row_of(pl, first) - back;
+        const S *src = g.in[K] + t0 * g.ldin[K] + c0 + u;
+        S *dst = reinterpret_cast<S *>(rows_of<K>(st) + first * 8) + u;
+        const int64_t step = (REV ? -g.ldin[K] : g.ldin[K]) * ROWS;
+        const int lo = pl.lo - first, hi = (int)min((int64_t)pl.hi, back ? row_of(pl, 0) : (int64_t)C) - first;
+        const int left = (int)min(g.n_chan - c0 - u, (int64_t)P::W);
+        if constexpr (U * sizeof(S) >= 4) {
+            const int bytes = min(left, U) * (int)sizeof(S);
 #pragma unroll
-        for (int i = 0; i < R; ++i, src += step) {
-            const int p = p0 + i;
-            if (p < pl.lo || p >= pl.hi || (back && t0 - i < 0))
-                continue;
-            S *dst = reinterpret_cast<S *>(rows_of<K>(st) + p * 8 + l8);
+            for (int i = 0; i < 16; i += ROWS, src += step, dst += ROWS * P::W)
+                if (i >= lo && i < hi && left > 0)
+                    copy_async<U * (int)sizeof(S)>(dst, src, bytes);
+        } else {
+            constexpr int N = 8;                           // rows in flight
+#pragma unroll 1
+            for (int i0 = 0; i0 < 16; i0 += N, src += N * step, dst += N * P::W) {
+                S x[N][TURNS];
 #pragma unroll
-            for (int u = 0; u < V; u += U) {
-                if (u >= left)
-                    continue;
-                if constexpr (U * sizeof(S) >= 4)
-                    copy_async<U * (int)sizeof(S)>(dst + u, src + u, (int)min(left - u, (int64_t)U) * (int)sizeof(S));
-                else
-                    dst[u] = src[u];
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int k = 0; k < TURNS; ++k)
+                        if (i0 + i >= lo && i0 + i < hi && k * LANES < left)
+                            x[i][k] = src[i * step + k * LANES];
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int k = 0; k < TURNS; ++k)
+                        if (i0 + i >= lo && i0 + i < hi && k * LANES < left)
+                            dst[i * P::W + k * LANES] = x[i][k];
             }
         }
+    }
+    // this thread's copies, or its plain stores, are there
+    static __device__ __forceinline__ void arrive(unsigned long long *bar)
+    {
+        if constexpr (U * sizeof(S) >= 4)
+            mbar_arrive_after_copies(bar);
+        else
+            mbar_arrive(bar);
     }
     // what pass 1 reads of tile j, and what only pass 2 reads: by one thread (BOX) or all compute threads
     __device__ __forceinline__ void load(const TilePlan &pl, int j)
@@ -535,7 +561,7 @@ struct Recur {
         else {
             copy_rows<0>(pl, j % P::NZ);
             copy_rows<1>(pl, j % P::N1S);
-            mbar_arrive_after_copies(&sm.full[j % P::N1S]);
+            arrive(&sm.full[j % P::N1S]);
         }
     }
     __device__ __forceinline__ void load_late(const TilePlan &pl, int j)
@@ -549,7 +575,7 @@ struct Recur {
                 copy_rows<2>(pl, j % P::NX);
                 if constexpr (P::NIN > 3)
                     copy_rows<3>(pl, j % P::NX);
-                mbar_arrive_after_copies(&sm.late[j % P::NX]);
+                arrive(&sm.late[j % P::NX]);
             }
         }
     }
@@ -568,9 +594,39 @@ struct Recur {
     {
         unpack16(reads(K) ? rows_of<K>(st)[stage_row(p0 + i) * 8 + l8] : make_uint4(0, 0, 0, 0), x, S());
     }
-    __device__ __forceinline__ A enter_of(int s, int64_t ch) const
+    // One row of states (n_chan fp32 or fp64 values), the thread's channels of it: 16 bytes at a time where that is
+    // aligned; zeros where there is none.
+    __device__ __forceinline__ bool wide_states(const A *p, int64_t c) const
     {
-        return g.enter && ch < g.n_chan ? g.enter[(int64_t)s * g.n_chan + ch] : A(0);
+        return ((uintptr_t)p | (uintptr_t)(g.n_chan * (int64_t)sizeof(A))) % 16 == 0 && c + V <= g.n_chan;
+    }
+    __device__ __forceinline__ void get_states(const A *p, int s, int64_t c, A (&x)[V]) const
+    {
+        if (p && wide_states(p, c)) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(p + (int64_t)s * g.n_chan + c);
+            uint4 r[V / Q];
+#pragma unroll
+            for (int j = 0; j < V / Q; ++j)
+                r[j] = q[j];
+            memcpy(x, r, sizeof(r));
+        } else
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                x[v] = p && c + v < g.n_chan ? p[(int64_t)s * g.n_chan + c + v] : A(0);
+    }
+    __device__ __forceinline__ void put_states(A *p, int s, int64_t c, const A (&x)[V]) const
+    {
+        if (wide_states(p, c)) {
+            uint4 r[V / Q];
+            memcpy(r, x, sizeof(r));
+#pragma unroll
+            for (int j = 0; j < V / Q; ++j)
+                reinterpret_cast<uint4 *>(p + (int64_t)s * g.n_chan + c)[j] = r[j];
+        } else
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (c + v < g.n_chan)
+                    p[(int64_t)s * g.n_chan + c + v] = x[v];
     }
 
     // What a thread keeps of its coefficients between the passes: a; of a sigmoid the smaller of a and 1 - a, negative
@@ -604,6 +660,7 @@ struct Recur {
     __device__ __forceinline__ void pass1_rows(const TilePlan &pl, int slot, int sz, int st, Kept &kp, A (&ma)[V], A (&mh)[V])
     {
         const int64_t c0 = (int64_t)pl.cb * P::W;
+        bool cut = false;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             A z[V], x[V];
@@ -619,10 +676,10 @@ struct Recur {
             A a[V], w[V], y[V];
             gates_of<GATE, sizeof(S) == 2>(z, a, w);
             keep(kp.k[i], a, w);
-            if (SEG && s >= 0)                             // what enters the row by name
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    mh[v] = enter_of(s, c0 + chan(v));
+            if (SEG && s >= 0) {                           // a sequence begins
+                get_states(g.enter, s, c0 + l8 * V, mh);
+                cut = true;
+            }
             const bool first = i == 0 && !(SEG && s >= 0);
             if constexpr (!REV) {
                 if constexpr (GATE == SLA_GATE_SIGMOID)
@@ -641,26 +698,21 @@ struct Recur {
                     vmul(mh, a, y);
                 }
             }
-            if constexpr (SEG) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    A m = i == 0 ? a[v] + A(0) : product(a[v], ma[v]);
-                    if (s >= 0)
-                        m = const_mark<A>();
-                    if (!inside) {
-                        m = const_mark<A>();
-                        mh[v] = A(0);
-                    }
-                    ma[v] = m;
-                }
-            } else if (i == 0)
+            if (SEG && !inside) {
+                vset(mh, A(0));
+                cut = true;
+            }
+            if (i == 0)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     ma[v] = a[v];
             else
                 vmul(ma, ma, a);
         }
-        if constexpr (!SEG) {                              // -0 marks a constant map
+        // -0 marks a constant map
+        if (SEG && cut)
+            vset(ma, const_mark<A>());
+        else {
             A zero[V];
             vset(zero, A(0));
             vadd(ma, ma, zero);
@@ -762,9 +814,7 @@ struct Recur {
             staged<1>(st, i, y);
             kept(kp.k[i], a, w);
             if (SEG && s >= 0)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    x[v] = enter_of(s, c0 + chan(v));
+                get_states(g.enter, s, c0 + l8 * V, x);
             if constexpr (!REV) {
                 if constexpr (GATE == SLA_GATE_SIGMOID)
                     vmul(y, w, y);
@@ -774,11 +824,7 @@ struct Recur {
                 A hb[V], lam[V];
                 staged<2>(sx, i, hb);
                 if (SEG && f >= 0)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const int64_t ch = c0 + chan(v);
-                        hb[v] = g.before && ch < g.n_chan ? g.before[(int64_t)f * g.n_chan + ch] : A(0);
-                    }
+                    get_states(g.before, f, c0 + l8 * V, hb);
                 vadd(lam, y, x);
                 vmul(x, a, lam);
                 if constexpr (GATE == SLA_GATE_SIGMOID) {
@@ -800,14 +846,8 @@ struct Recur {
                 if (g.out[1])
                     store(1, i, t, c0, st, sx, hb);
             }
-            if (SEG && f >= 0 && g.leave) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int64_t ch = c0 + chan(v);
-                    if (ch < g.n_chan)
-                        g.leave[(int64_t)f * g.n_chan + ch] = x[v];
-                }
-            }
+            if (SEG && f >= 0 && g.leave)
+                put_states(g.leave, f, c0 + l8 * V, x);
         }
     }
 
@@ -841,9 +881,10 @@ struct Recur {
             q.h[k] = sm.mapH[buf][r0 + k][place];
         }
     }
-    // (A, H) of the runs in q behind (ta, th).  PLAIN: no borders in the tile, so no map is constant, and in A's own
-    // type without the guard against an overflowed A times 0; where the tile's result is not finite it is
-    // taken again with both, and with the product in fp64 (of four runs each, 16 coefficients).
+    // (A, H) of the runs in q behind (ta, th).  PLAIN: in A's own type, a constant map's -0 as the factor 0 that it
+    // is.  That is right as long as everything is finite, and leaves a result that is not where it is not (infinity
+    // times 0); then it is taken again with constant maps and zero states looked at, and the product
+    // in fp64 (of four runs each, 16 coefficients).
     template <bool PLAIN, typename T>
     static __device__ __forceinline__ void compose(const Runs &q, T &ta, A &th)
     {
@@ -869,7 +910,8 @@ struct Recur {
             compose<PLAIN>(q, ta, th);
         }
     }
-    // Every run gets the map of the runs in front of it.
+    // Every run gets the map of the runs in front of it.  CUT: behind a constant map all are; GUARD: compose()'s.
+    template <bool CUT, bool GUARD>
     __device__ __forceinline__ void front_maps(int buf, int place, Runs &q)
     {
         A fa = A(1), fh = A(0);
@@ -880,13 +922,32 @@ struct Recur {
             for (int k = 0; k < HELD; ++k) {
                 sm.mapA[buf][r0 + k][place] = fa;
                 sm.mapH[buf][r0 + k][place] = fh;
-                fh = fma_of(q.a[k], fh, q.h[k]);
-                fa = fma_of(fa, q.a[k], A(0));             // -0 marks a constant map
+                fh = GUARD ? apply(q.a[k], fh, q.h[k]) : fma_of(q.a[k], fh, q.h[k]);
+                if (CUT && (is_const(fa) || is_const(q.a[k])))
+                    fa = const_mark<A>();
+                else
+                    fa = fma_of(fa, q.a[k], A(0));         // -0 marks a constant map
             }
         }
     }
-    // Every run gets the constant map of the state that enters it, from x: with borders in the tile, or where
-    // products leave the range.
+    // whether their products stay in A's range
+    __device__ __forceinline__ bool fronts_fit(int buf, int place, Runs &q) const
+    {
+        A fa = A(1);
+        bool fit = true;
+        for (int r0 = 0; r0 < P::NR; r0 += HELD) {
+            if (HELD < P::NR)
+                take(buf, place, r0, q);
+#pragma unroll
+            for (int k = 0; k < HELD; ++k) {
+                fa = product(q.a[k], fa);
+                fit = fit && !isinf(fa);
+            }
+        }
+        return fit;
+    }
+    // Every run gets the constant map of the state that enters it, from x, run by run: where products of
+    // coefficients leave A's range.
     __device__ __forceinline__ void front_states(int buf, int place, A x)
     {
         for (int r0 = 0; r0 < P::NR; r0 += 4) {
@@ -904,33 +965,24 @@ struct Recur {
             }
         }
     }
-    // whether the runs' maps may be composed in their own type: no borders, everything finite
-    static __device__ __forceinline__ bool plain(const TilePlan &pl, typename Words<A>::Map pa, A th)
-    {
-        return !pl.seg && Words<A>::finite(pa) && isfinite(th);
-    }
-
     // one channel of a tile: its map, published
     __device__ __forceinline__ void maps(const TilePlan &pl, int buf, int place, Runs &q)
     {
         using Wd = Words<A>;
         const int64_t ch = (int64_t)pl.cb * P::W + chan_at(place);
-        A th = A(0);
-        typename Wd::Map pa = Wd::pack(A(1));
-        bool ok = !pl.seg;
+        A ta, th;
         if (HELD == P::NR)
             take(buf, place, 0, q);
-        if (ok) {
-            A ta;
-            tile_map<true>(buf, place, q, ta, th);
-            pa = Wd::pack(ta + A(0));
-            ok = isfinite(ta) && isfinite(th);
+        tile_map<true>(buf, place, q, ta, th);
+        typename Wd::Map pa = Wd::pack(pl.cut ? const_mark<A>() : ta + A(0));
+        const bool plain = isfinite(ta) && isfinite(th);
+        if (!plain) {
+            double wa;
+            tile_map<false>(buf, place, q, wa, th);
+            pa = Wd::pack(wa);
         }
-        if (!ok) {
-            double ta;
-            tile_map<false>(buf, place, q, ta, th);
-            pa = Wd::pack(ta);
-        }
+        // 0: a state warp goes through the runs
+        sm.fronts[buf][place] = plain ? (pl.cut ? 2 : 1) : fronts_fit(buf, place, q) ? 3 : 0;
         sm.tileA[buf][place] = pa;
         sm.tileH[buf][place] = th;
         if (pl.chunk + 1 < g.n_chunks && ch < g.n_chan) {
@@ -955,7 +1007,7 @@ struct Recur {
         if (ch >= g.n_chan)
             return A(0);
         if (pl.first >= 0)
-            return enter_of(pl.first, ch);
+            return g.enter ? g.enter[(int64_t)pl.first * g.n_chan + ch] : A(0);
         if (!enters(pl))
             return A(0);
         return state_before<A>(pl.chunk, g.n_chan, ch, g.n_cb * 4 < (int)gridDim.x, g.agg, (const typename Words<A>::Inc *)g.inc);
@@ -972,7 +1024,7 @@ struct Recur {
             return;
         if (pl.chunk + 1 < g.n_chunks && !Wd::fixed(pa))
             st_word((typename Wd::Inc *)g.inc + (int64_t)pl.chunk * g.n_chan + ch, Wd::inc_bits(Wd::apply(pa, x, th)));
-        if (!plain(pl, pa, th))
+        if (!sm.fronts[buf][place])
             front_states(buf, place, x);
     }
 
@@ -1029,7 +1081,7 @@ struct Recur {
         const int64_t v0 = min(max(lo, r0), r1), v1 = max(v0, min(hi, r1));
         pl.lo = (int)(REV ? r1 - v1 : v0 - r0);
         pl.hi = (int)(REV ? r1 - v0 : v1 - r0);
-        bool seg = pl.lo > 0 || pl.hi < C, cleared = false;
+        bool seg = pl.lo > 0 || pl.hi < C, cut = seg, cleared = false;
         int first = -1;
         for (int64_t s = s0;; s += 32) {
             const int64_t mine = s + lane;
@@ -1052,7 +1104,8 @@ struct Recur {
             const unsigned at0 = __ballot_sync(0xffffffffu, in == 0);
             if (at0)
                 first = (int)(s + __ffs(at0) - 1);
-            const bool any = __any_sync(0xffffffffu, in > 0 || leave >= 0);
+            cut = __any_sync(0xffffffffu, in > 0) || cut;
+            const bool any = cut || __any_sync(0xffffffffu, leave >= 0);
             if ((any || seg) && !cleared) {
                 for (int p = lane; p < C; p += 32)
                     sm.begin[slot][p] = sm.finish[slot][p] = -1;
@@ -1067,6 +1120,7 @@ struct Recur {
                 break;
         }
         pl.first = first;
+        pl.cut = cut;
         pl.seg = seg;
         if (lane == 0)
             sm.plan[slot] = pl;
@@ -1088,12 +1142,14 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
     constexpr int NS = P::NS, NP = P::NP;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     RecurSmem<S, GATE, REV> &sm = *reinterpret_cast<RecurSmem<S, GATE, REV> *>(smem_raw);
-    K r(g, sm);
+    // The warps that the others wait for come first: a scheduler with several warps ready takes the oldest.
+    constexpr int STATE = P::NK, PLAN = 2 * P::NK, COMPUTE = PLAN + 32;
+    K r(g, sm, (int)threadIdx.x - COMPUTE);
     constexpr int RUNS = P::NC + P::NK, TILE = 2 * P::NK, ENTER = P::NC + 2 * P::NK + 32, START = P::NC + 32;
     auto up = [](int x, int n) { return x + 1 == n ? 0 : x + 1; };
-    const int place = (r.tid - P::NC) % P::NK;             // of map and state threads
+    const int place = threadIdx.x % P::NK;                 // of map and state threads
 
-    if (r.tid < P::NC) {                                   // compute warps
+    if (threadIdx.x >= COMPUTE) {                          // compute warps
         typename K::Kept now, next;
         // while the first plan is made: empty sequences leave with what entered them
         if (g.leave && (g.q.off || g.q.n_tokens == 0))
@@ -1144,7 +1200,7 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
         }
         if constexpr (!K::BOX)
             asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (r.tid < P::NC + P::NK) {                    // map warps
+    } else if (threadIdx.x < STATE) {                      // map warps
         bar_sync(BAR_FIRST, P::NT);
         for (int slot = 0, odd = 0;; slot = up(slot, NP), odd ^= 1) {
             bar_sync(BAR_RUNS + odd, RUNS);
@@ -1156,12 +1212,19 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
                 r.maps(pl, odd, place, q);
             __syncwarp();
             bar_arrive(BAR_TILE + odd, TILE);
-            if (place < P::W && K::plain(pl, sm.tileA[odd][place], sm.tileH[odd][place]))
-                r.front_maps(odd, place, q);
+            if (place < P::W) {
+                const int how = sm.fronts[odd][place];
+                if (how == 1)
+                    r.template front_maps<false, false>(odd, place, q);
+                else if (how == 2)
+                    r.template front_maps<true, false>(odd, place, q);
+                else if (how == 3)
+                    r.template front_maps<true, true>(odd, place, q);
+            }
             __syncwarp();
             bar_arrive(BAR_ENTER + odd, ENTER);
         }
-    } else if (r.tid < P::NC + 2 * P::NK) {                // state warps
+    } else if (threadIdx.x < PLAN) {                       // state warps
         bar_sync(BAR_FIRST, P::NT);
         for (int slot = 0, odd = 0;; slot = up(slot, NP), odd ^= 1) {
             const TilePlan &pl = sm.plan[slot];            // there since the barriers of the tile before

@@ -647,7 +647,7 @@ sla_status launch_dw(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
 template <typename S, int U>
 sla_status launch_unit(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
 {
-    constexpr int M = U * sizeof(S) == 16 ? 1 : 2;
+    constexpr int M = U * sizeof(S) == 16 ? 1 : U * sizeof(S) > 2 ? 2 : 4;
     if (g.top_k <= 2)
         return launch_dw<S, U, 2, 2 * M>(g, to_slots, s);
     if (g.top_k <= 4)
