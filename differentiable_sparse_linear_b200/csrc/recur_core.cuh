@@ -1157,10 +1157,18 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
                 if (g.q.at(s + 1) <= g.q.at(s))
                     for (int64_t c = r.tid; c < g.n_chan; c += P::NC)
                         g.leave[s * g.n_chan + c] = g.enter ? g.enter[s * g.n_chan + c] : A(0);
+        __syncwarp();
         bar_sync(BAR_FIRST, P::NT);                        // plan 0
         if constexpr (!K::BOX) {
             r.load(sm.plan[0], 0);
             r.load_late(sm.plan[0], 0);
+            __syncwarp();
+        }
+        // Plan 1 comes before the map warps hear of tile 0: the state warps look at it once they have tile 0's map.
+        bar_sync(BAR_START, START);
+        if constexpr (!K::BOX) {
+            r.load(sm.plan[1], 1);
+            r.load_late(sm.plan[1], 1);
         }
         if (sm.plan[0].tile >= 0) {
             r.loaded(0);
@@ -1168,14 +1176,10 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
         }
         __syncwarp();
         bar_arrive(BAR_RUNS, RUNS);
-        for (int j = 1; j < NS; ++j) {
-            bar_sync(BAR_START, START);                    // the plans of the next tiles
-            if constexpr (!K::BOX) {
-                r.load(sm.plan[j], j);
-                if (j == 1)
-                    r.load_late(sm.plan[1], 1);
-                __syncwarp();
-            }
+        bar_sync(BAR_START, START);                        // plan 2; its stage of input 0 is free after pass 1 of tile 0
+        if constexpr (!K::BOX) {
+            r.load(sm.plan[2], 2);
+            __syncwarp();
         }
         int slot = 0;
         for (int i = 0; sm.plan[slot].tile >= 0; ++i) {
@@ -1227,7 +1231,9 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
     } else if (threadIdx.x < PLAN) {                       // state warps
         bar_sync(BAR_FIRST, P::NT);
         for (int slot = 0, odd = 0;; slot = up(slot, NP), odd ^= 1) {
-            const TilePlan &pl = sm.plan[slot];            // there since the barriers of the tile before
+            // Plan j is there once tile j - 1's map is: that waits for its runs, and the compute warps hand those over
+            // after the barrier that brought plan j (the first for j = 0, the start for 1 and 2, ENTER j - 3).
+            const TilePlan &pl = sm.plan[slot];
             if (pl.tile < 0)
                 break;
             A x = A(0);

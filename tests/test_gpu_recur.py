@@ -327,6 +327,28 @@ def test_same_bits_every_time():
         assert all(torch.equal(p, q) for p, q in zip(first, now))
 
 
+@pytest.mark.parametrize("channels", [1024, 1022])
+def test_many_sequences_many_times(channels):
+    """Thousands of short sequences over several tiles a block, again and again: where borders lie takes longer to find
+    than a tile's work, so every hand-over between a block's warps is met in another order."""
+    tokens, seqs = 12000, 3000
+    g = torch.Generator().manual_seed(1)
+    cuts = torch.randint(0, tokens + 1, (seqs - 1,), generator=g).sort().values
+    off = torch.cat([torch.tensor([0]), cuts, torch.tensor([tokens])]).tolist()
+    x = data((tokens, off), channels, torch.bfloat16, "exp")
+    few = [0, 5, 1023]
+    h, last = sla.sla_recur_solve(x["a"], x["b"], x["h0"], x["off"], gate="exp")
+    few = [c for c in few if c < channels]
+    sub = {k: (v[:, few].contiguous() if torch.is_tensor(v) and v.dim() == 2 else v) for k, v in x.items()}
+    check_solve(sub, h[:, few], last[:, few], "exp", torch.bfloat16)
+    got = sla.sla_recur_adjoint(x["a"], h, x["dh"], h0=x["h0"], seq_off=x["off"], dh_last=x["dlast"], gate="exp")
+    for _ in range(40):
+        again = sla.sla_recur_solve(x["a"], x["b"], x["h0"], x["off"], gate="exp")
+        assert torch.equal(again[0], h) and torch.equal(again[1], last)
+        back = sla.sla_recur_adjoint(x["a"], h, x["dh"], h0=x["h0"], seq_off=x["off"], dh_last=x["dlast"], gate="exp")
+        assert all(torch.equal(s, t) for s, t in zip(back, got))
+
+
 def test_streams_and_graphs():
     """On a stream given or current, captured, replayed on new inputs, two captured calls at the same time."""
     x = data((9000, [0, 4000, 9000]), 72, torch.bfloat16, "exp")
