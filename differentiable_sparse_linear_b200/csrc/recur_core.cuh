@@ -1028,8 +1028,23 @@ struct Recur {
             front_states(buf, place, x);
     }
 
+    // What the plan warp keeps from tile to tile: the ticket drawn ahead, the first and last row of all sequences, and
+    // where the last tile's first sequence was.
+    struct PlanState {
+        unsigned ticket = 0;
+        int64_t lo = 0, hi = 0, hint = 0;
+    };
+    __device__ __forceinline__ void start(PlanState &ps) const
+    {
+        if (g.ticket && lane == 0)
+            ps.ticket = atomicAdd(g.ticket, 1u);
+        if (g.q.n_seq > 0) {
+            ps.lo = g.q.at(0);
+            ps.hi = max(ps.lo, g.q.at(g.q.n_seq));
+        }
+    }
     // the plan warp: the next tile, and where sequences begin and end in it
-    __device__ __forceinline__ bool plan(int slot, int k)
+    __device__ __forceinline__ bool plan(int slot, int k, PlanState &ps)
     {
         TilePlan pl;
         const int64_t tiles = (int64_t)g.n_chunks * g.n_cb;
@@ -1037,10 +1052,9 @@ struct Recur {
         if (k > 0 && tiles <= gridDim.x)                   // a tile a block
             tile = tiles;
         else if (g.ticket) {
-            unsigned v = 0;
-            if (lane == 0)
-                v = atomicAdd(g.ticket, 1u) + 1u;          // the counter starts at all bits set
-            tile = __shfl_sync(0xffffffffu, v, 0);
+            tile = __shfl_sync(0xffffffffu, ps.ticket + 1u, 0);   // the counter starts at all bits set
+            if (lane == 0 && tiles > gridDim.x)
+                ps.ticket = atomicAdd(g.ticket, 1u);
         } else
             tile = blockIdx.x + (int64_t)k * gridDim.x;
         if (tile >= tiles) {
@@ -1056,45 +1070,42 @@ struct Recur {
         const int64_t pos1 = min(n, pos0 + C);
         // the tile's rows in row order
         const int64_t r0 = REV ? n - pos1 : pos0, r1 = REV ? n - pos0 : pos1;
-        // the offsets of up to 31 sequences in one look, or the first one that ends behind r0 by 32 probes at a time
         const int32_t n_seq = g.q.n_seq;
-        const bool few = n_seq < 32;
-        int64_t off = few && lane <= n_seq && n_seq > 0 ? g.q.at(lane) : INT64_MAX;
-        int64_t lo, hi, s0 = 0;
-        if (few) {
-            lo = n_seq > 0 ? __shfl_sync(0xffffffffu, off, 0) : 0;
-            hi = n_seq > 0 ? __shfl_sync(0xffffffffu, off, n_seq) : 0;
-        } else {
-            lo = g.q.at(0);
-            hi = g.q.at(n_seq);
-            int64_t s1 = n_seq;                            // it is in [s0, s1]
-            while (s1 - s0 > 32) {
-                const int64_t step = (s1 - s0 + 31) / 32;
-                const int64_t s = min(s0 + step * (lane + 1) - 1, s1 - 1);
-                const unsigned behind = __ballot_sync(0xffffffffu, g.q.at(s + 1) > r0);
-                const int64_t b0 = s0 + step * (behind ? __ffs(behind) - 1 : 31);
-                s1 = behind ? min(s1, b0 + step - 1) : s1;
-                s0 = behind ? min(b0, s1) : s1;
-            }
-        }
-        hi = max(lo, hi);
+        const int64_t lo = ps.lo, hi = ps.hi;
         const int64_t v0 = min(max(lo, r0), r1), v1 = max(v0, min(hi, r1));
         pl.lo = (int)(REV ? r1 - v1 : v0 - r0);
         pl.hi = (int)(REV ? r1 - v0 : v1 - r0);
+        // Offsets are looked at 32 at a time, 31 sequences, from near where the last tile's first one was.  The window
+        // is right if nothing in front of it ends behind r0 and something in it does; else the first one
+        // that does is searched for, 32 probes at a time.
+        int64_t w = n_seq < 32 ? 0 : min(max(ps.hint - (REV ? 24 : 0), (int64_t)0), (int64_t)n_seq - 31);
+        auto look = [&] { return w + lane <= n_seq && n_seq > 0 ? g.q.at(w + lane) : INT64_MAX; };
+        int64_t off = look();
+        const unsigned behind = __ballot_sync(0xffffffffu, lane > 0 && w + lane <= n_seq && off > r0);
+        const int64_t off0 = __shfl_sync(0xffffffffu, off, 0);
+        if (behind && (w == 0 || off0 <= r0))
+            ps.hint = w + __ffs(behind) - 2;
+        else if (n_seq >= 32) {
+            int64_t s0 = 0, s1 = n_seq;                    // it is in [s0, s1]
+            while (s1 - s0 > 32) {
+                const int64_t step = (s1 - s0 + 31) / 32;
+                const int64_t s = min(s0 + step * (lane + 1) - 1, s1 - 1);
+                const unsigned later = __ballot_sync(0xffffffffu, g.q.at(s + 1) > r0);
+                const int64_t b0 = s0 + step * (later ? __ffs(later) - 1 : 31);
+                s1 = later ? min(s1, b0 + step - 1) : s1;
+                s0 = later ? min(b0, s1) : s1;
+            }
+            ps.hint = w = s0;
+            off = look();
+        }
         bool seg = pl.lo > 0 || pl.hi < C, cut = seg, cleared = false;
         int first = -1;
-        for (int64_t s = s0;; s += 32) {
-            const int64_t mine = s + lane;
+        for (;;) {
+            const int64_t mine = w + lane, next = __shfl_down_sync(0xffffffffu, off, 1);
             int64_t b = INT64_MAX, e = -1;
-            if (few) {
-                const int64_t next = __shfl_down_sync(0xffffffffu, off, 1);
-                if (lane < n_seq) {
-                    b = off;
-                    e = next - 1;
-                }
-            } else if (mine < n_seq) {
-                b = g.q.at(mine);
-                e = g.q.at(mine + 1) - 1;                  // last row
+            if (lane < 31 && mine < n_seq) {
+                b = off;
+                e = next - 1;                              // last row
             }
             const bool full = mine < n_seq && e >= b;
             const bool bin = full && b >= r0 && b < r1, ein = full && e >= r0 && e < r1;
@@ -1103,7 +1114,7 @@ struct Recur {
             const int in = REV ? (ein ? pe : -1) : (bin ? pb : -1), leave = REV ? (bin ? pb : -1) : (ein ? pe : -1);
             const unsigned at0 = __ballot_sync(0xffffffffu, in == 0);
             if (at0)
-                first = (int)(s + __ffs(at0) - 1);
+                first = (int)(w + __ffs(at0) - 1);
             cut = __any_sync(0xffffffffu, in > 0) || cut;
             const bool any = cut || __any_sync(0xffffffffu, leave >= 0);
             if ((any || seg) && !cleared) {
@@ -1116,8 +1127,10 @@ struct Recur {
                 sm.begin[slot][in] = (int)mine;
             if (leave >= 0)
                 sm.finish[slot][leave] = (int)mine;
-            if (s + 32 >= n_seq || __all_sync(0xffffffffu, b >= r1))
+            if (w + 31 >= n_seq || __all_sync(0xffffffffu, b >= r1))
                 break;
+            w += 31;
+            off = look();
         }
         pl.first = first;
         pl.cut = cut;
@@ -1250,6 +1263,8 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
         // The compute warps take NS plans before their loop and one in every turn of it, when they are done with the
         // tile before and with pass 1 of the next one: the stages of tile j are free.
         int slot = 0, end = INT32_MAX, odd = 0;
+        typename K::PlanState ps;
+        r.start(ps);
         if (r.lane == 0) {
             for (int m = 0; m < P::N1S; ++m)
                 mbar_init(&sm.full[m], K::BOX ? 1 : P::NC);
@@ -1261,7 +1276,7 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
         __syncwarp();
         for (int j = 0; j < end; ++j) {
             if (end == INT32_MAX) {
-                if (!r.plan(slot, j))
+                if (!r.plan(slot, j, ps))
                     end = j + NS;
             } else if (r.lane == 0)
                 sm.plan[slot].tile = -1;
