@@ -691,7 +691,7 @@ sla_status check_route(int32_t dtype, int64_t n_tokens, int32_t top_k, int64_t n
 
 sla_status check_rows(const void *p, int64_t ld, int64_t n_rows, int64_t n_chan, bool out)
 {
-    if (n_rows == 0)
+    if (n_rows == 0 || n_chan == 0)
         return SLA_SUCCESS;
     if (!p || (ld < n_chan && (out || ld != 0)))
         return fail(SLA_ERR_INVALID_ARG, "NULL rows, or a row stride below the number of channels");

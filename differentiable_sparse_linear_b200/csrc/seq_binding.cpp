@@ -102,6 +102,8 @@ int32_t gate_code(PyObject *o)
 int64_t row_stride(const at::Tensor &t)
 {
     const int64_t dim = t.dim(), d = t.size(dim - 1);
+    if (t.numel() == 0)
+        return d;
     if (d > 1 && t.stride(dim - 1) != 1)
         return -1;
     int64_t ld, n;
@@ -138,6 +140,14 @@ int64_t rows(const at::Tensor &t, const at::Tensor &like, const char *name, bool
     if (out && ld < t.size(t.dim() - 1))
         refuse(name, ": an output's rows must not overlap");
     return ld;
+}
+
+// An output may share a buffer with the inputs (columns of it), but not be one of them.
+void apart(const at::Tensor *out, std::initializer_list<const at::Tensor *> others, const char *name)
+{
+    for (const at::Tensor *t : others)
+        if (out && t && out->numel() > 0 && t->numel() > 0 && out->data_ptr() == t->data_ptr())
+            refuse(name, " must not be one of the other arguments");
 }
 
 // Checks a contiguous tensor of the given sizes; its pointer (NULL for none).
@@ -234,6 +244,8 @@ PyObject *recur_solve(PyObject *const *p)
     void *p0 = plain(h0, states, wide(b), b, "h0");
     int64_t ldh = out ? rows(*out, b, "out", true) : q.channels;
     plain(h_last, states, wide(b), b, "h_last");
+    apart(out, {&a, &b, h0, h_last}, "out");
+    apart(h_last, {&a, &b, h0}, "h_last");
     const Place here(b);
     const at::Tensor h = out ? *out : here.make(b.sizes());
     const at::Tensor last = h_last ? *h_last : here.make(states, wide(b));
@@ -271,6 +283,8 @@ PyObject *recur_adjoint(PyObject *const *p)
         refuse("give both da and db, or neither");
     int64_t ldda = want_da && given ? rows(*da, h, "da", true) : q.channels;
     int64_t lddb = want_db && given ? rows(*db, h, "db", true) : q.channels;
+    apart(da, {&a, &h, dh, b, h0, dlast, db}, "da");
+    apart(db, {&a, &h, dh, b, h0, dlast}, "db");
     const Place here(h);
     at::Tensor oa, ob, o0, work;
     if (want_da)
@@ -310,6 +324,8 @@ PyObject *recur_step(PyObject *const *p)
         refuse("without index every row needs a slot");
     void *pi = plain(index, {n}, at::kInt, b, "index");
     const int64_t ldh = out ? rows(*out, b, "out", true) : channels;
+    apart(out, {&a, &b, &state}, "out");
+    apart(&state, {&a, &b}, "state");
     const Place here(b);
     const at::Tensor h = out ? *out : here.make(b.sizes());
     check(sla_recur_step(code, gate, n, channels, state.size(0), a.data_ptr(), lda, b.data_ptr(), ldb, state.data_ptr(), lds,
@@ -390,6 +406,7 @@ PyObject *route_to_slots(PyObject *const *p)
     const int64_t ldx = side(x, r.tokens, x, "rows"), channels = x.size(1), pairs[2] = {r.tokens, r.top_k};
     void *pw = plain(weight, pairs, wide(x), x, "weight");
     const int64_t ldys = ys ? side(*ys, r.slots, x, "ys") : 0, ldo = out ? side(*out, r.slots, x, "out", true) : channels;
+    apart(out, {&x, ys, weight}, "out");
     const Place here(x);
     const at::Tensor xs = out ? *out : here.make({r.slots, channels});
     const uint32_t flags = out ? 0 : SLA_FILL_REST;
@@ -419,6 +436,7 @@ PyObject *route_to_tokens(PyObject *const *p)
     const int64_t ldys = side(ys, r.slots, ys, "rows"), channels = ys.size(1), pairs[2] = {r.tokens, r.top_k};
     void *pw = plain(weight, pairs, wide(ys), ys, "weight");
     const int64_t ldx = x ? side(*x, r.tokens, ys, "x") : 0, ldo = out ? side(*out, r.tokens, ys, "out", true) : channels;
+    apart(out, {&ys, x, weight}, "out");
     const Place here(ys);
     const at::Tensor y = out ? *out : here.make({r.tokens, channels});
     at::Tensor dw;

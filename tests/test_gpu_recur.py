@@ -403,6 +403,22 @@ def test_rows_beyond_32_bit_offsets():
     assert torch.equal(buf[:, 3000:3000 + d], da) and torch.equal(buf[:, 4000:4000 + d], db)
 
 
+def test_nothing_to_do():
+    """No tokens, no channels, no sequences; first states pass through to the last ones."""
+    z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    h0 = torch.rand(3, 8, device="cuda")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    assert torch.equal(sla.sla_recur_solve(z(0, 8), z(0, 8), h0, off)[1], h0)
+    assert torch.equal(sla.sla_recur_solve(z(3, 0, 8), z(3, 0, 8), h0)[1], h0)
+    assert [t.shape for t in sla.sla_recur_solve(z(0, 5, 8), z(0, 5, 8))] == [(0, 5, 8), (0, 8)]
+    assert [t.shape for t in sla.sla_recur_solve(z(5, 0), z(5, 0))] == [(5, 0), (1, 0)]
+    da, db, dh0 = sla.sla_recur_adjoint(z(0, 8), z(0, 8), None, h0=h0, seq_off=off, dh_last=2 * h0)
+    assert da.shape == db.shape == (0, 8) and torch.equal(dh0, 2 * h0)
+    assert sla.sla_recur_step(z(0, 8), z(0, 8), z(0, 8)).shape == (0, 8)
+    h = sla.sla_recur_step(z(2, 8) + 1, z(2, 8) + 1, z(0, 8), torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert (h == 0).all()
+
+
 def test_offsets_out_of_range_stay_inside():
     """Offsets beyond the rows lead to no access outside them (results of such a call are unspecified)."""
     x = data("ragged", 16, torch.float32, "value")

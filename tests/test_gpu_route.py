@@ -171,6 +171,17 @@ def test_strided_rows(kind):
             check_pattern(dw2, p, kind)
 
 
+def test_nothing_to_do():
+    z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    r = sla.sla_route_sort(torch.zeros(4, 2, dtype=torch.int64, device="cuda"), 3)
+    assert sla.sla_route_dispatch(z(4, 0), r).shape == (8, 0) and sla.sla_route_combine(z(8, 0), r).shape == (4, 0)
+    assert (sla.sla_route_combine_adjoint(z(4, 0), r, z(8, 0))[1] == 0).all()
+    assert (sla.sla_route_dispatch_adjoint(z(8, 0), r, z(4, 0))[1] == 0).all()
+    r = sla.sla_route_sort(torch.zeros(0, 2, dtype=torch.int64, device="cuda"), 3, align=4)
+    assert r.offsets.tolist() == [0, 0, 0, 0] and (r.entry == -1).all()
+    assert (sla.sla_route_dispatch(z(0, 8), r) == 0).all() and sla.sla_route_combine(z(9, 8), r).shape == (0, 8)
+
+
 def test_slots_out_of_range_stay_inside():
     """A plan whose slots lead outside the rows reads and writes nothing there."""
     p = problem(20, 2, 4, 32, 1, 0, torch.float32)

@@ -161,7 +161,7 @@ def test_cpu_tensors_are_refused(native):
     ids = torch.zeros(4, dtype=torch.int32)
     route = plan()
     for call in (lambda: sla.sla_recur_solve(x, x), lambda: sla.recurrence(x, x), lambda: sla.sla_recur_adjoint(x, x, x),
-                 lambda: sla.sla_recur_step(x, x, x), lambda: sla.sla_route_sort(ids, 3),
+                 lambda: sla.sla_recur_step(x, x, x.clone()), lambda: sla.sla_route_sort(ids, 3),
                  lambda: sla.sla_route_dispatch(x, route), lambda: sla.sla_route_combine(x, route),
                  lambda: sla.route_dispatch(x, route), lambda: sla.route_combine(x, route),
                  lambda: sla.sla_recur_solve(a=x, b=x, h0=s), lambda: sla.sla_recur_solve([1.0], [2.0]),
@@ -188,7 +188,7 @@ def test_row_strides(native):
 
 
 def test_recurrence_refuses(native):
-    x = torch.zeros(4, 8)
+    x, y = torch.zeros(4, 8), torch.zeros(4, 8)
     off = torch.tensor([0, 4], dtype=torch.int32)
     solve, adjoint, step = sla.sla_recur_solve, sla.sla_recur_adjoint, sla.sla_recur_step
     for call, words in [
@@ -216,9 +216,13 @@ def test_recurrence_refuses(native):
             (lambda: step(x, x, x[:3]), "slot"),
             (lambda: step(x, x, x.bfloat16()), "state must be"),
             (lambda: step(x, x, x[:1].expand(4, 8)), "overlap"),
-            (lambda: step(x, x, x, torch.arange(4)), "index must be"),
-            (lambda: step(x, x, x, torch.zeros(3, dtype=torch.int32)), "index must be"),
-            (lambda: step(x[None], x[None], x), "rows must be")]:
+            (lambda: step(x, x, y, torch.arange(4)), "index must be"),
+            (lambda: step(x, x, y, torch.zeros(3, dtype=torch.int32)), "index must be"),
+            (lambda: step(x[None], x[None], x), "rows must be"),
+            (lambda: solve(x, y, out=y), "other arguments"),
+            (lambda: solve(x, y, torch.zeros(1, 8), h_last=x[:1]), "other arguments"),
+            (lambda: adjoint(x, y, y, da=y, db=x.clone()), "other arguments"),
+            (lambda: step(x, y, x), "other arguments")]:
         with pytest.raises(ValueError, match=words):
             call()
     for bad in (off.long(), off[:0], off[None], torch.zeros(6, dtype=torch.int32)[::2]):
@@ -245,6 +249,8 @@ def test_routing_refuses(native):
             (lambda: sla.sla_route_dispatch(x.t(), plan(tokens=8)), "stride"),
             (lambda: sla.sla_route_dispatch(x, r, w.double()), "weight must be"),
             (lambda: sla.sla_route_dispatch(x, r, w[:, 0]), "weight must be"),
+            (lambda: sla.sla_route_dispatch(x, r, out=x), "other arguments"),
+            (lambda: sla.sla_route_combine(x, r, out=x), "other arguments"),
             (lambda: sla.sla_route_dispatch(x, r, out=x[:3]), "out must be"),
             (lambda: sla.sla_route_dispatch(x, r, out=x[:1].expand(4, 8)), "overlap"),
             (lambda: sla.sla_route_dispatch(x, sla.Route(r.offsets, r.counts, r.entry, r.slot.long())), "route.slot"),
