@@ -9,7 +9,8 @@ namespace {
 constexpr int RT = 128;
 
 // One row for each sequence of a serving batch.  A thread takes V channels of a row: 16 bytes of a, b and h where
-// everything is aligned to it, one value otherwise.  Bound by memory: 3 values and a state in and out a channel.
+// everything is aligned to it, one value otherwise.  Bound by memory: 3 values and a state in and out a channel;
+// 384 x 4096 bf16 take 4.3 us (22 MB, floor 3.4), one value a thread took 8.8.
 template <typename S, int GATE, int V>
 __global__ void __launch_bounds__(RT)
     k_recur_step(int64_t n_rows, int64_t n_chan, int64_t n_slots, const S *a, int64_t lda, const S *b, int64_t ldb,

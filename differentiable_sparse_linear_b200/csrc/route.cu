@@ -21,9 +21,12 @@ constexpr int MAX_EXPERTS = 4096;
 //
 // Up to one tile of entries (8192 at 256 experts) one block does all of it in one launch.  Above, blocks rank
 // their runs and leave histograms, and a second launch adds what lies in front: two launches of up
-// to 148 blocks, each a pass over the ids.
+// to 148 blocks, each a pass over the ids.  Latency bounds it, not memory (131072 x 8 ids: 17 MB, 2.6 us):
+// 18 us there, 11 us for 8192 entries, 3.2 us for 64.  Votes over the expert's bits rank a warp in 21 us where
+// match_any took 25; entries written from the order in shared memory 18 where scattered ones took 21.
 constexpr int ST = 1024;                      // threads at most
 constexpr int IT = 8;                         // entries of a lane in a tile
+constexpr int SORTED = ST * IT;               // entries that a block puts in order in shared memory
 
 template <typename I>
 __device__ __forceinline__ int expert_of(I v, int n_experts)
@@ -90,11 +93,13 @@ __device__ __forceinline__ void write_plan(int n_experts, int align, int64_t n_s
         entry[p] = -1;
 }
 
-// Shared memory: per-warp counts (16 bits: a tile has at most 8192 entries), two arrays of sums, the offsets.
+// Shared memory: per-warp counts (16 bits: a tile has at most 8192 entries), two arrays of sums, the offsets, and for
+// one block alone with more than 1024 entries those in order.
 static inline int sort_warps(int n_experts) { return std::max(1, std::min(ST / 32, (128 << 10) / (2 * n_experts))); }
-static inline size_t sort_smem(int n_experts, int warps)
+static inline size_t sort_smem(int n_experts, int warps, bool staged)
 {
-    return ((size_t)warps * n_experts * 2 + 15) / 16 * 16 + sizeof(int) * (3 * (size_t)n_experts + 1);
+    return ((size_t)warps * n_experts * 2 + 15) / 16 * 16 + sizeof(int) * (3 * (size_t)n_experts + 1) +
+           (staged ? sizeof(int) * ((size_t)n_experts + 1 + SORTED) : 0);
 }
 
 template <typename I, bool ALONE>
@@ -109,6 +114,8 @@ __global__ void __launch_bounds__(ST)
     int *run = reinterpret_cast<int *>(smem + (cells * 2 + 15) / 16 * 16);   // entries of the expert in earlier tiles
     int *sum = run + n_experts;                                             // ... up to this tile
     int *off = sum + n_experts;
+    int *front = off + n_experts + 1;
+    uint32_t *sorted = reinterpret_cast<uint32_t *>(front + n_experts + 1);
     const int64_t b0 = min(n, per_block * blockIdx.x), b1 = min(n, b0 + per_block);
     const int bits = 32 - __clz(n_experts);
     for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
@@ -154,21 +161,33 @@ __global__ void __launch_bounds__(ST)
             sum[e] += acc;
         }
         __syncthreads();
-        if constexpr (ALONE)
+        // Alone, entries of one expert are put next to one another first (k_route_place has the reason).
+        const bool staged = ALONE && n > 1024;
+        if constexpr (ALONE) {
             padded_offsets(n_experts, align, sum, off);
+            if (staged)
+                padded_offsets(n_experts, 1, sum, front);
+        }
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int64_t e = e0 + 32 * i;
             if (x[i] >= 0) {
                 const int p = (ALONE ? off[x[i]] : run[x[i]]) + mine[x[i]] + rank[i];
                 slot[e] = p;
-                if (ALONE)
+                if (staged)
+                    sorted[front[x[i]] + p - off[x[i]]] = (uint32_t)x[i] << 16 | (uint32_t)e;
+                else if (ALONE)
                     entry[p] = (int)e;
             } else if (x[i] == -1)
                 slot[e] = -1;
         }
         __syncthreads();
     }
+    if (ALONE && n > 1024)
+        for (int q = threadIdx.x; q < front[n_experts]; q += blockDim.x) {
+            const int x = (int)(sorted[q] >> 16);
+            entry[off[x] + q - front[x]] = (int)(sorted[q] & 0xffffu);
+        }
     if constexpr (ALONE)
         write_plan(n_experts, align, n_slots, sum, off, 0, 1, offsets, counts, entry);
     else
@@ -183,7 +202,8 @@ __global__ void __launch_bounds__(ST)
                   int32_t *offsets, int32_t *counts, int32_t *entry, int32_t *slot, const int32_t *hist)
 {
     extern __shared__ __align__(16) unsigned char smem[];
-    int *cnt = reinterpret_cast<int *>(smem), *base = cnt + n_experts, *off = base + n_experts;
+    int *cnt = reinterpret_cast<int *>(smem), *base = cnt + n_experts, *off = base + n_experts, *front = off + n_experts + 1;
+    uint32_t *sorted = reinterpret_cast<uint32_t *>(front + n_experts + 1);   // (expert, entry of the block) by expert
     const int64_t b0 = min(n, per_block * blockIdx.x), b1 = min(n, b0 + per_block);
     // totals and what lies in front, `parts` threads an expert
     const int parts = max(1, (int)blockDim.x / n_experts);
@@ -205,6 +225,9 @@ __global__ void __launch_bounds__(ST)
         }
     __syncthreads();
     padded_offsets(n_experts, align, cnt, off);
+    const bool one_tile = per_block <= SORTED;
+    if (one_tile)
+        padded_offsets(n_experts, 1, hist + (size_t)blockIdx.x * n_experts, front);
     for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
         base[e] += off[e];
     __syncthreads();
@@ -222,8 +245,19 @@ __global__ void __launch_bounds__(ST)
             if (x[i] >= 0) {
                 const int p = base[x[i]] + r[i];
                 slot[e] = p;
-                entry[p] = (int)e;
+                if (one_tile)
+                    sorted[front[x[i]] + r[i]] = (uint32_t)x[i] << 16 | (uint32_t)(e - b0);
+                else
+                    entry[p] = (int)e;
             }
+        }
+    }
+    // entries of one expert next to one another, so that neighbouring threads write neighbouring slots
+    if (one_tile) {
+        __syncthreads();
+        for (int q = threadIdx.x; q < front[n_experts]; q += blockDim.x) {
+            const int x = (int)(sorted[q] >> 16);
+            entry[base[x] + q - front[x]] = (int)(b0 + (sorted[q] & 0xffffu));
         }
     }
     write_plan(n_experts, align, n_slots, cnt, off, blockIdx.x, gridDim.x, offsets, counts, entry);
@@ -241,8 +275,15 @@ static inline int64_t sort_blocks(int64_t n, int n_experts)
 // One group of G threads a token, a row cut into units of U values (16 bytes where all rows are aligned to
 // it).  A token's row crosses memory once: read and written to each of its slots, or summed from them;
 // the gradient on the pattern is the dot product of the rows that pass anyway.  Sums run over j in
-// order and over the channels in an order fixed by n_chan and the rows' alignment, so results do not
+// order and over the channels in an order fixed by the sizes and the rows' alignment, so results do not
 // depend on scheduling.
+//
+// Memory bounds all four: 16384 tokens x 2 choices x 4096 bf16 take 70 us for R^T x (0.88 of the copy rate on 403 MB),
+// 74 for R y (0.84), 111 and 102 with the gradient on the pattern (0.93, 0.80).  What carried them: 16-byte units,
+// KU x NV of them in flight a thread, the plan's slots and weights once a thread, up to four turns a
+// thread (one turn: R y 87 us), K sums shared out over the lanes (K butterflies: 134 us for R y with its gradient),
+// kernels without dot products apart (38 registers instead of 128: R^T x 100 us before).  Rows not aligned
+// to 4 bytes go value by value: 4097 channels, R^T x 135 us, R y 178.
 constexpr int PT = 256;
 
 template <typename S, int U>
@@ -744,12 +785,11 @@ sla_status sla_route_sort(int64_t n_tokens, int32_t top_k, int32_t n_experts, in
         return fail(SLA_ERR_INVALID_ARG, "d_work is NULL, smaller than sla_route_workspace_bytes or not 16-byte aligned");
     cudaStream_t s = (cudaStream_t)stream;
     const int warps = sort_warps(n_experts);
-    const size_t smem = sort_smem(n_experts, warps);
-    // with few entries only the warps that have some
     const int64_t blocks = sort_blocks(n, n_experts);
-    auto allow = [&](auto kernel) -> sla_status {
-        if (smem > 48 << 10)
-            SLA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    const size_t smem = sort_smem(n_experts, warps, blocks == 1 && n > 1024);
+    auto allow = [&](auto kernel, size_t bytes) -> sla_status {
+        if (bytes > 48 << 10)
+            SLA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
         return SLA_SUCCESS;
     };
     auto run = [&](auto ids) -> sla_status {
@@ -758,17 +798,17 @@ sla_status sla_route_sort(int64_t n_tokens, int32_t top_k, int32_t n_experts, in
             // few entries: a lane takes one, as long as there are warps
             const int w = (int)std::min<int64_t>(warps, std::max<int64_t>({1, (n + 31) / 32, ((int64_t)n_experts + 31) / 32}));
             const int turns = (int)std::max<int64_t>(1, (n + 32 * w - 1) / (32 * w));
-            SLA_TRY(allow(k_route_rank<I, true>));
+            SLA_TRY(allow(k_route_rank<I, true>, smem));
             k_route_rank<I, true><<<1, 32 * w, smem, s>>>(n, n, turns, n_experts, align, ids, n_slots, d_offsets, d_counts,
                                                          d_entry, d_slot, nullptr);
         } else {
             const int64_t tile = (int64_t)warps * 32 * IT, per = ((n + blocks - 1) / blocks + tile - 1) / tile * tile;
             const unsigned grid = (unsigned)((n + per - 1) / per);
-            SLA_TRY(allow(k_route_rank<I, false>));
+            SLA_TRY(allow(k_route_rank<I, false>, smem));
             k_route_rank<I, false><<<grid, 32 * warps, smem, s>>>(n, per, IT, n_experts, align, ids, n_slots, d_offsets,
                                                                  d_counts, d_entry, d_slot, (int32_t *)d_work);
-            const size_t smem2 = sizeof(int) * (3 * (size_t)n_experts + 1);
-            SLA_TRY(allow(k_route_place<I>));
+            const size_t smem2 = sizeof(int) * (4 * (size_t)n_experts + 2 + SORTED);
+            SLA_TRY(allow(k_route_place<I>, smem2));
             k_route_place<I><<<grid, ST, smem2, s>>>(n, per, n_experts, align, ids, n_slots, d_offsets, d_counts,
                                                      d_entry, d_slot, (const int32_t *)d_work);
         }

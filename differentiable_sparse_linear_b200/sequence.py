@@ -15,10 +15,13 @@ Rows are [tokens, channels] tensors of float32, float64, bfloat16 or float16 who
 contiguous; rows may be strided, and an input's rows may be one row expanded.  States, weights
 and their gradients are float32 (float64 with float64 rows).  The work runs on the current
 stream of the tensors' device, or on ``stream``, in whose memory pool outputs and scratch memory
-are then allocated.  Nothing synchronises; every call can be captured into a CUDA graph, and a
-graph's scratch memory belongs to its own pool.  Inside a capture use the sla_* calls or
-``torch.autograd.grad`` on tensors made inside it: ``backward()`` onto leaves that an eager
-graph still holds makes torch's engine join that graph's stream, which a capture cannot do.
+are then allocated.  Outputs must not be inputs.
+
+Nothing synchronises, and every call can be captured into a CUDA graph; a graph's scratch memory
+belongs to its own pool, so graphs may be replayed at the same time.  A captured backward pass must not
+share leaves with an eager graph that is still alive: torch's engine would join the eager
+stream, and the capture fails with an error.  Drop the eager graph first, or capture over
+``detach().requires_grad_()`` of the leaves.
 """
 from __future__ import annotations
 

@@ -32,7 +32,7 @@ SORTS = [
     (0, 2, 4, 1, 0), (1, 1, 1, 1, 0), (1, 1, 5, 1, 1.0), (1, 8, 64, 16, 0), (7, 3, 5, 4, 0.2), (16, 4, 64, 1, 0),
     (31, 1, 2, 1, 0), (33, 2, 300, 128, 0.1), (1000, 2, 8, 128, 0.05), (1024, 1, 1, 1, 0), (4097, 3, 17, 1, 0.3),
     (5000, 8, 256, 64, 0), (20011, 5, 100, 1, 0.01), (300, 2, 4096, 2, 0), (9000, 4, 4096, 1, 0.1), (65536, 8, 128, 128, 0),
-    (200000, 2, 33, 1, 0), (70000, 1, 1000, 8, 0.5),
+    (200000, 2, 33, 1, 0), (70000, 1, 1000, 8, 0.5), (1500, 2, 4096, 2, 0.1), (250000, 5, 40, 1, 0.02),
 ]
 
 
