@@ -353,24 +353,24 @@ struct Window {
 };
 
 // The state that enters `chunk` at one channel: back to the nearest chunk whose leaving state is there, then
-// forward over the maps behind it, one after the other.  Four chunks a look, or 16 (fp64: 8) from the start where
-// more than four chunks are at work at a time (`deep`).
-template <typename A>
-__device__ __forceinline__ A state_before(int chunk, int64_t n_chan, int64_t ch, bool deep, const unsigned long long *agg,
+// forward over the maps behind it, one after the other.  FIRST chunks at the first look and while their maps are
+// missing, 16 (fp64: 8) further back.
+template <typename A, int FIRST>
+__device__ __forceinline__ A state_before(int chunk, int64_t n_chan, int64_t ch, const unsigned long long *agg,
                                           const typename Words<A>::Inc *inc)
 {
     constexpr int K = 16 / Words<A>::N, LIMIT = 1 << 22;
     A x = A(0);
-    int polls = 0, got = -1, last = chunk - 1;
-    if (!deep) {
-        Window<A, 4> near;
+    int polls = 0, got, last = chunk - 1;
+    {
+        Window<A, FIRST> near;
         do {
             near.load(last, n_chan, ch, agg, inc);
             got = near.look(last, x);
         } while (got == 0 && ++polls < LIMIT);
         if (got > 0)
             return x;
-        last -= 4;
+        last -= FIRST;
     }
     Window<A, K> far;
     while (got <= 0 && polls < LIMIT && last >= 0) {
@@ -893,37 +893,26 @@ struct Recur {
             q.h[k] = sm.mapH[buf][r0 + k][place];
         }
     }
-    // (A, H) of the runs in q behind (ta, th).  PLAIN: in A's own type, a constant map's -0 as the factor 0 that it
-    // is.  That is right as long as everything is finite, and leaves a result that is not where it is not (infinity
-    // times 0); then it is taken again with constant maps and zero states looked at, and the product
-    // in fp64 (of four runs each, 16 coefficients).
-    template <bool PLAIN, typename T>
-    static __device__ __forceinline__ void compose(const Runs &q, T &ta, A &th)
+    // The tile's (A, H) in A's own type, a constant map's -0 as the factor 0 that it is.  That is right as long as
+    // everything is finite, and leaves a result that is not where it is not (infinity times 0).
+    __device__ __forceinline__ void tile_map(int buf, int place, Runs &q, A &ta, A &th) const
     {
-#pragma unroll
-        for (int k = 0; k < HELD; k += 4) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                th = PLAIN ? fma_of(q.a[k + e], th, q.h[k + e]) : apply(q.a[k + e], th, q.h[k + e]);
-            if constexpr (PLAIN)
-                ta *= (q.a[k] * q.a[k + 1]) * (q.a[k + 2] * q.a[k + 3]);
-            else
-                ta = product((T)product(product(q.a[k + 3], q.a[k + 2]), product(q.a[k + 1], q.a[k])), ta);
-        }
-    }
-    template <bool PLAIN, typename T>
-    __device__ __forceinline__ void tile_map(int buf, int place, Runs &q, T &ta, A &th) const
-    {
-        ta = T(1);
+        ta = A(1);
         th = A(0);
         for (int r0 = 0; r0 < P::NR; r0 += HELD) {
             if (HELD < P::NR)
                 take(buf, place, r0, q);
-            compose<PLAIN>(q, ta, th);
+#pragma unroll
+            for (int k = 0; k < HELD; k += 4) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    th = fma_of(q.a[k + e], th, q.h[k + e]);
+                ta *= (q.a[k] * q.a[k + 1]) * (q.a[k + 2] * q.a[k + 3]);
+            }
         }
     }
-    // Every run gets the map of the runs in front of it.  CUT: behind a constant map all are; GUARD: compose()'s.
-    template <bool CUT, bool GUARD>
+    // Every run gets the map of the runs in front of it.  CUT: behind a constant map all are.
+    template <bool CUT>
     __device__ __forceinline__ void front_maps(int buf, int place, Runs &q)
     {
         A fa = A(1), fh = A(0);
@@ -934,7 +923,7 @@ struct Recur {
             for (int k = 0; k < HELD; ++k) {
                 sm.mapA[buf][r0 + k][place] = fa;
                 sm.mapH[buf][r0 + k][place] = fh;
-                fh = GUARD ? apply(q.a[k], fh, q.h[k]) : fma_of(q.a[k], fh, q.h[k]);
+                fh = fma_of(q.a[k], fh, q.h[k]);
                 if (CUT && (is_const(fa) || is_const(q.a[k])))
                     fa = const_mark<A>();
                 else
@@ -942,26 +931,46 @@ struct Recur {
             }
         }
     }
-    // whether their products stay in A's range
-    __device__ __forceinline__ bool fronts_fit(int buf, int place, Runs &q) const
+    // Both again where the tile's result is not finite, with constant maps and zero states looked at and the product in
+    // fp64 (of four runs each, 16 coefficients); rare, and out of the way of the others' code.  `fit`: the
+    // front maps' products stay in A's range.
+    static __device__ __noinline__ void guarded_map(const Sm &sm, int buf, int place, double &wa, A &th, bool &fit)
     {
+        wa = 1.0;
+        th = A(0);
         A fa = A(1);
-        bool fit = true;
-        for (int r0 = 0; r0 < P::NR; r0 += HELD) {
-            if (HELD < P::NR)
-                take(buf, place, r0, q);
+        fit = true;
+#pragma unroll 1
+        for (int r = 0; r < P::NR; r += 4) {
+            A m = A(1);
 #pragma unroll
-            for (int k = 0; k < HELD; ++k) {
-                fa = product(q.a[k], fa);
+            for (int e = 0; e < 4; ++e) {
+                const A a = sm.mapA[buf][r + e][place];
+                th = apply(a, th, sm.mapH[buf][r + e][place]);
+                m = product(a, m);
+                fa = product(a, fa);
                 fit = fit && !isinf(fa);
             }
+            wa = product((double)m, wa);
         }
-        return fit;
+    }
+    static __device__ __noinline__ void guarded_fronts(Sm &sm, int buf, int place)
+    {
+        A fa = A(1), fh = A(0);
+#pragma unroll 1
+        for (int r = 0; r < P::NR; ++r) {
+            const A a = sm.mapA[buf][r][place], h = sm.mapH[buf][r][place];
+            sm.mapA[buf][r][place] = fa;
+            sm.mapH[buf][r][place] = fh;
+            fh = apply(a, fh, h);
+            fa = product(a, fa);
+        }
     }
     // Every run gets the constant map of the state that enters it, from x, run by run: where products of
     // coefficients leave A's range.
-    __device__ __forceinline__ void front_states(int buf, int place, A x)
+    static __device__ __noinline__ void front_states(Sm &sm, int buf, int place, A x)
     {
+#pragma unroll 1
         for (int r0 = 0; r0 < P::NR; r0 += 4) {
             A a[4], h[4];
 #pragma unroll
@@ -985,16 +994,17 @@ struct Recur {
         A ta, th;
         if (HELD == P::NR)
             take(buf, place, 0, q);
-        tile_map<true>(buf, place, q, ta, th);
+        tile_map(buf, place, q, ta, th);
         typename Wd::Map pa = Wd::pack(pl.cut ? const_mark<A>() : ta + A(0));
-        const bool plain = isfinite(ta) && isfinite(th);
-        if (!plain) {
+        int how = pl.cut ? 2 : 1;
+        if (!(isfinite(ta) && isfinite(th))) {
             double wa;
-            tile_map<false>(buf, place, q, wa, th);
+            bool fit;
+            guarded_map(sm, buf, place, wa, th, fit);
             pa = Wd::pack(wa);
+            how = fit ? 3 : 0;                             // 0: a state warp goes through the runs
         }
-        // 0: a state warp goes through the runs
-        sm.fronts[buf][place] = plain ? (pl.cut ? 2 : 1) : fronts_fit(buf, place, q) ? 3 : 0;
+        sm.fronts[buf][place] = (unsigned char)how;
         sm.tileA[buf][place] = pa;
         sm.tileH[buf][place] = th;
         if (pl.chunk + 1 < g.n_chunks && ch < g.n_chan) {
@@ -1022,7 +1032,16 @@ struct Recur {
             return g.enter ? g.enter[(int64_t)pl.first * g.n_chan + ch] : A(0);
         if (!enters(pl))
             return A(0);
-        return state_before<A>(pl.chunk, g.n_chan, ch, g.n_cb * 4 < (int)gridDim.x, g.agg, (const typename Words<A>::Inc *)g.inc);
+        // A look waits longer the more words it loads: four chunks where about as many are at work at a time (16384 x
+        // 4096 bf16, 64 channel tiles: 106 us, with eight 113, with 16 160), eight where it is more (32768 x 2560, 40
+        // tiles: 132 us, with four and then 16 163), 16 where it is far more (40000 x 304, 5 tiles: 56 us, with eight 60).
+        const typename Words<A>::Inc *inc = (const typename Words<A>::Inc *)g.inc;
+        const int n = (int)gridDim.x;
+        if (g.n_cb * 5 >= n * 2)
+            return state_before<A, 4>(pl.chunk, g.n_chan, ch, g.agg, inc);
+        if (g.n_cb * 12 >= n)
+            return state_before<A, 8>(pl.chunk, g.n_chan, ch, g.agg, inc);
+        return state_before<A, 16 / Words<A>::N>(pl.chunk, g.n_chan, ch, g.agg, inc);
     }
     // its leaving state, published, and where the maps do not compose the runs' states
     __device__ __forceinline__ void hand_over(const TilePlan &pl, int buf, int place, A x)
@@ -1037,7 +1056,7 @@ struct Recur {
         if (pl.chunk + 1 < g.n_chunks && !Wd::fixed(pa))
             st_word((typename Wd::Inc *)g.inc + (int64_t)pl.chunk * g.n_chan + ch, Wd::inc_bits(Wd::apply(pa, x, th)));
         if (!sm.fronts[buf][place])
-            front_states(buf, place, x);
+            front_states(sm, buf, place, x);
     }
 
     // What the plan warp keeps from tile to tile: the ticket drawn ahead, the first and last row of all sequences, and
@@ -1244,11 +1263,11 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
             if (place < P::W) {
                 const int how = sm.fronts[odd][place];
                 if (how == 1)
-                    r.template front_maps<false, false>(odd, place, q);
+                    r.template front_maps<false>(odd, place, q);
                 else if (how == 2)
-                    r.template front_maps<true, false>(odd, place, q);
+                    r.template front_maps<true>(odd, place, q);
                 else if (how == 3)
-                    r.template front_maps<true, true>(odd, place, q);
+                    K::guarded_fronts(sm, odd, place);
             }
             __syncwarp();
             bar_arrive(BAR_ENTER + odd, ENTER);
