@@ -38,15 +38,15 @@
 //
 // What bounds it.  Memory must carry z, b and h once (backward z, g, h, dz, db): 6 (10) bytes a value in 16 bits.  The
 // kernel moves little more (380 of 403 MB at 16384 x 4096 bf16, forward, besides 8 + 4 bytes a channel and chunk
-// of published words) but runs at 0.55 to 0.6 of the copy rate there, 105 us, 0.65 in fp32 (92 us), backward 0.65 (160 us)
-// and 0.76 (134 us): about 23 instructions a value at 42 % of the issue slots.  Warps wait for one another's results once
-// a tile and for fixed latencies in between; 16 warps of 128 registers are all that fit.  Measured on the way
+// of published words) but runs at 0.55 to 0.6 of the copy rate there, 105 us, 0.66 in fp32 (16384 x 2048, 93 us),
+// backward 0.6 (170 us) and 0.79 (130 us): about 23 instructions a value at 39 % of the issue slots.  Warps wait for
+// one another's results once a tile and for fixed latencies in between; 16 warps of 128 registers are all that fit.  Measured on the way
 // (solve 65536 x 4096 bf16): every gate twice instead of kept coefficients and combining runs by shuffles 655 us,
 // maps by the scan warps 532, four scan threads a channel 501, tensor copies, kept coefficients and paired
-// arithmetic 455, first states as entering states 424.  Rows of 128 bytes by a bulk copy each took 185 us where tensor
+// arithmetic 455, first states as entering states 424, guards out of line 403.  Rows of 128 bytes by a bulk copy each took 185 us where tensor
 // copies take 105 (16384 x 4096); copies by one warp's cp.async 171; runs of 8 rows by 7 warps 157; two blocks of half a
 // tile an SM 215.  Few channels leave few chunks side by side and the chain of chunks bounds: 200000 x 64 bf16 takes
-// 108 us of a floor of 12.  Tiles with borders cost half as much again (16384 x 4096 in 100 sequences: 161 us).
+// 106 us of a floor of 12.  Tiles with borders cost half as much again (16384 x 4096 in 100 sequences: 161 us).
 //
 // A sequence border inside a run makes its map constant.  Such a map is marked by A = -0 (products are
 // normalised to +0), because 0 * x would carry a NaN or an infinity across the border.  Where the entering state is
@@ -1378,7 +1378,8 @@ bool box_map(CUtensorMap *map, const S *p, int64_t n_tokens, int64_t n_chan, int
 
 // By alignment: tensor copies where every array's rows are aligned to 16 bytes and every input has a stride (a row
 // expanded over the tokens has none); else units of 4 bytes (two of a 16-bit type) or one value.  Copies
-// below 4 bytes are not asynchronous.
+// below 4 bytes are not asynchronous.  16384 rows of 1000, 1002 and 1001 bf16: 54, 71 and 132 us; of 1024 and 1001
+// fp32: 58 and 91 us.
 template <typename S, int GATE, bool REV>
 sla_status launch_recur(RecurArgs<S> &g, cudaStream_t s)
 {
