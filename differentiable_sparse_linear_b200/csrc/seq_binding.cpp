@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstring>
 #include <sstream>
 #include <stdexcept>
@@ -142,12 +143,39 @@ int64_t rows(const at::Tensor &t, const at::Tensor &like, const char *name, bool
     return ld;
 }
 
-// An output may share a buffer with the inputs (columns of it), but not be one of them.
+// The bytes of checked rows: n of `width` bytes, `pitch` apart.
+struct Extent {
+    uintptr_t first;
+    int64_t n, width, pitch;
+    explicit Extent(const at::Tensor &t) : first((uintptr_t)t.data_ptr())
+    {
+        const int64_t d = t.dim() > 0 ? t.size(t.dim() - 1) : 1, ld = t.dim() > 1 ? row_stride(t) : d;
+        n = d > 0 ? t.numel() / d : 0;
+        if (ld == 0)                                       // one row for all
+            n = std::min<int64_t>(n, 1);
+        width = d * t.element_size();
+        pitch = ld * t.element_size();
+    }
+    uintptr_t last() const { return first + (uintptr_t)((n - 1) * pitch + width); }
+};
+bool overlap(const Extent &x, const Extent &y)
+{
+    if (x.n == 0 || y.n == 0 || x.last() <= y.first || y.last() <= x.first)
+        return false;
+    if (x.n == 1 ? y.n == 1 : y.n > 1 && x.pitch != y.pitch)
+        return true;                                       // two runs of bytes, or rows not told apart
+    // columns of one buffer: y's rows start behind x's within the pitch and end before the next one
+    const int64_t pitch = x.n > 1 ? x.pitch : y.pitch, apart = (int64_t)(y.first - x.first) % pitch;
+    const int64_t at = apart < 0 ? apart + pitch : apart;
+    return at < x.width || at + y.width > pitch;
+}
+
+// An output may share a buffer with the inputs (columns or other rows of it), but not memory.
 void apart(const at::Tensor *out, std::initializer_list<const at::Tensor *> others, const char *name)
 {
     for (const at::Tensor *t : others)
-        if (out && t && out->numel() > 0 && t->numel() > 0 && out->data_ptr() == t->data_ptr())
-            refuse(name, " must not be one of the other arguments");
+        if (out && t && overlap(Extent(*out), Extent(*t)))
+            refuse(name, " must not share memory with the other arguments");
 }
 
 // Checks a contiguous tensor of the given sizes; its pointer (NULL for none).
@@ -201,6 +229,8 @@ Sequences sequences(const at::Tensor &b, const at::Tensor *seq_off)
     if (b.dim() == 3) {
         if (seq_off)
             refuse("seq_off goes with packed [tokens, channels] rows");
+        if (b.size(0) > INT32_MAX)
+            refuse("too many sequences");
         return {b.size(0) * b.size(1), b.size(2), (int32_t)b.size(0), nullptr};
     }
     if (b.dim() != 2)
@@ -283,8 +313,9 @@ PyObject *recur_adjoint(PyObject *const *p)
         refuse("give both da and db, or neither");
     int64_t ldda = want_da && given ? rows(*da, h, "da", true) : q.channels;
     int64_t lddb = want_db && given ? rows(*db, h, "db", true) : q.channels;
-    apart(da, {&a, &h, dh, b, h0, dlast, db}, "da");
-    apart(db, {&a, &h, dh, b, h0, dlast}, "db");
+    const at::Tensor *to_a = want_da ? da : nullptr, *to_b = want_db ? db : nullptr, *in_b = reads_b ? b : nullptr;
+    apart(to_a, {&a, &h, dh, in_b, h0, dlast, to_b}, "da");
+    apart(to_b, {&a, &h, dh, in_b, h0, dlast}, "db");
     const Place here(h);
     at::Tensor oa, ob, o0, work;
     if (want_da)
@@ -302,8 +333,8 @@ PyObject *recur_adjoint(PyObject *const *p)
                             h0 ? o0.data_ptr() : nullptr, given ? 0 : SLA_FILL_REST, size ? work.data_ptr() : nullptr, size,
                             here.stream),
           "sla_recur_adjoint");
-    written(da);
-    written(db);
+    written(to_a);
+    written(to_b);
     return tuple({wrap_or_none(oa), wrap_or_none(ob), wrap_or_none(o0)});
 }
 
@@ -466,6 +497,15 @@ PyObject *stride_of(PyObject *const *p)
     return PyLong_FromLongLong(ld);
 }
 
+// x, y -> whether their rows share memory
+PyObject *share_memory(PyObject *const *p)
+{
+    const at::Tensor &x = need(p[0], "x"), &y = need(p[1], "y");
+    rows(x, x, "x");
+    rows(y, y, "y");
+    return PyBool_FromLong(overlap(Extent(x), Extent(y)));
+}
+
 PyObject *set_error_types(PyObject *const *p)
 {
     Py_INCREF(p[0]);
@@ -503,7 +543,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 
 #define ENTRY(f, n) {#f, (PyCFunction)(void (*)(void))entry<f, n>, METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {ENTRY(recur_solve, 7), ENTRY(recur_adjoint, 12), ENTRY(recur_step, 6), ENTRY(route_sort, 4),
-                           ENTRY(route_to_slots, 8), ENTRY(route_to_tokens, 8), ENTRY(stride_of, 1), ENTRY(set_error_types, 2),
+                           ENTRY(route_to_slots, 8), ENTRY(route_to_tokens, 8), ENTRY(stride_of, 1), ENTRY(share_memory, 2),
+                           ENTRY(set_error_types, 2),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_sla_seq", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

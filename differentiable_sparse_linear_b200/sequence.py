@@ -15,7 +15,8 @@ Rows are [tokens, channels] tensors of float32, float64, bfloat16 or float16 who
 contiguous; rows may be strided, and an input's rows may be one row expanded.  States, weights
 and their gradients are float32 (float64 with float64 rows).  The work runs on the current
 stream of the tensors' device, or on ``stream``, in whose memory pool outputs and scratch memory
-are then allocated.  Outputs must not be inputs.
+are then allocated.  Outputs must not share memory with inputs or with each other (different columns of
+one buffer do not).
 
 Nothing synchronises, and every call can be captured into a CUDA graph; a graph's scratch memory
 belongs to its own pool, so graphs may be replayed at the same time.  A captured backward pass must not

@@ -187,6 +187,41 @@ def test_row_strides(native):
     assert s(sequence._walkable(y.transpose(0, 1))) == 8
 
 
+def test_shared_memory(native):
+    shared = native.share_memory
+    x = torch.zeros(7, 12)
+    cases = [(x, x, True), (x[:4], x[4:], False), (x[:4], x[3:], True), (x[::2], x[1::2], False),
+             (x[:, :4], x[:, 4:], False), (x[:, 4:], x[:, :4], False), (x[:, :5], x[:, 4:], True),
+             (x[1:, :4], x[:-1, 4:], False), (x[1:, :5], x[:-1, 4:], True), (x[:, 8:], x[2:3, :8], False),
+             (x[:, 8:], x[2:3, :9], True), (x[2:3, :9], x[:, 8:], True), (x[:1, :3], x[:1, 3:], False),
+             (x[:1, :4], x[:1, 3:], True), (x[3:4].expand(5, 12), x[:4], True), (x[3:4].expand(5, 12), x[:3], False),
+             (x[:, :4], torch.zeros(7, 12), False), (x[::2], x[:, :4], True), (x[:0], x, False),
+             (x.view(-1)[:36].view(3, 12), x.view(-1)[30:66].view(3, 12), True)]
+    for p, q, expected in cases:
+        assert shared(p, q) is expected and shared(q, p) is expected
+        cells = [set((t.storage_offset() + (torch.arange(t.shape[0])[:, None] * t.stride(0) +
+                                            torch.arange(t.shape[1]) * t.stride(1))).flatten().tolist()) for t in (p, q)]
+        same = p.untyped_storage().data_ptr() == q.untyped_storage().data_ptr()
+        meet = same and bool(cells[0] & cells[1])
+        assert expected or not meet                        # what shares memory is never missed
+
+
+def test_shifted_rows_are_refused(native):
+    x = torch.zeros(9, 8)
+    y = torch.zeros(8, 8)
+    for call in (lambda: sla.sla_recur_solve(y, x[:-1], out=x[1:]),
+                 lambda: sla.sla_recur_solve(x[1:], y, out=x[:-1]),
+                 lambda: sla.sla_recur_adjoint(y, y, x[1:], da=x[:-1], db=y.clone()),
+                 lambda: sla.sla_recur_adjoint(y, y, y, da=x[1:], db=x[:-1]),
+                 lambda: sla.sla_recur_step(y, x[1:], x[:-1]),
+                 lambda: sla.sla_recur_solve(y, y, x[:1], out=x[:8])):
+        with pytest.raises(ValueError, match="other arguments"):
+            call()
+    wide = torch.zeros(8, 16)                              # columns of one buffer are not: these fail as CPU tensors
+    with pytest.raises(ValueError, match="CUDA"):
+        sla.sla_recur_solve(wide[:, :8], y, out=wide[:, 8:])
+
+
 def test_recurrence_refuses(native):
     x, y = torch.zeros(4, 8), torch.zeros(4, 8)
     off = torch.tensor([0, 4], dtype=torch.int32)
