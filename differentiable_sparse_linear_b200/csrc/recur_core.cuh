@@ -40,11 +40,11 @@
 // kernel moves little more (380 of 403 MB at 16384 x 4096 bf16, forward, besides 8 + 4 bytes a channel and chunk
 // of published words) but runs at 0.55 to 0.6 of the copy rate there, 105 us, 0.66 in fp32 (16384 x 2048, 93 us),
 // backward 0.6 (170 us) and 0.79 (130 us): about 23 instructions a value at 39 % of the issue slots.  Warps wait for
-// one another's results once a tile and for fixed latencies in between; 16 warps of 128 registers are all that fit.  Measured on the way
-// (solve 65536 x 4096 bf16): every gate twice instead of kept coefficients and combining runs by shuffles 655 us,
-// maps by the scan warps 532, four scan threads a channel 501, tensor copies, kept coefficients and paired
-// arithmetic 455, first states as entering states 424, guards out of line 403.  Rows of 128 bytes by a bulk copy each took 185 us where tensor
-// copies take 105 (16384 x 4096); copies by one warp's cp.async 171; runs of 8 rows by 7 warps 157; two blocks of half a
+// one another's results once a tile and for fixed latencies in between; 16 warps of 128 registers are all that fit.
+// Measured on the way (solve 65536 x 4096 bf16): every gate twice instead of kept coefficients and combining runs by
+// shuffles 655 us, maps by the scan warps 532, four scan threads a channel 501, tensor copies, kept coefficients and
+// paired arithmetic 455, first states as entering states 424, guards out of line 403.  Rows of 128 bytes by a bulk copy
+// each took 185 us where tensor copies take 105 (16384 x 4096); copies by one warp's cp.async 171; runs of 8 rows by 7 warps 157; two blocks of half a
 // tile an SM 215.  Few channels leave few chunks side by side and the chain of chunks bounds: 200000 x 64 bf16 takes
 // 106 us of a floor of 12.  Tiles with borders cost half as much again (16384 x 4096 in 100 sequences: 161 us).
 //
@@ -642,7 +642,7 @@ struct Recur {
     }
 
     // What a thread keeps of its coefficients between the passes: a; of a sigmoid the smaller of a and 1 - a, negative
-    // where that is 1 - a, so that both come back with all their digits.
+    // (its sign, for 1 - a may be 0) where that is 1 - a, so that both come back with all their digits.
     struct Kept {
         A k[R][V];
     };
@@ -657,9 +657,10 @@ struct Recur {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if constexpr (GATE == SLA_GATE_SIGMOID) {
-                const A rest = add_of(A(1), k[v] < A(0) ? k[v] : -k[v]);
-                a[v] = k[v] < A(0) ? rest : k[v];
-                w[v] = k[v] < A(0) ? -k[v] : rest;
+                const bool other = signbit(k[v]);
+                const A rest = add_of(A(1), other ? k[v] : -k[v]);
+                a[v] = other ? rest : k[v];
+                w[v] = other ? -k[v] : rest;
             } else {
                 a[v] = k[v];
                 w[v] = A(1);

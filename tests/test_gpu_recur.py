@@ -104,6 +104,42 @@ def test_long_sequence(kind, gate):
     check_adjoint(x, h, got, gate, kind)
 
 
+@pytest.mark.parametrize("kind", ref.KINDS)
+@pytest.mark.parametrize("gate", ["exp", "sigmoid"])
+@pytest.mark.parametrize("d", [64, 33])
+def test_gates_at_their_ends(kind, gate, d):
+    """Gates so far out that a coefficient or 1 minus it is 0, infinite ones among them.
+
+    Bound: besides the relative errors, a coefficient or weight below 2^-124 (fp64: 2^-1009) may be anything up to
+    that, where the arithmetic holds it or flushes it.  In 300 rows, values below 6 (asserted), |h| and |lambda| stay below
+    301 * 6 < 2^11, every product of the two below 2^22, and 300 such errors add up to less than
+    2^-124 * 2^22 * 2^9."""
+    kind = ref.KINDS[kind]
+    ends = [-float("inf"), -6e4, -1000.0, -200.0, -95.0, -88.0, -40.0, -17.0, -1.0, -0.0, 0.0]
+    if gate == "sigmoid":
+        ends += [-v for v in ends[:-2]]
+    x = data((300, [0, 7, 120, 290]), d, kind, gate)
+    pick = torch.randint(len(ends), x["a"].shape, generator=torch.Generator().manual_seed(d))
+    x["a"] = torch.tensor(ends, dtype=torch.float64)[pick].to(kind).cuda()
+    assert all(float(x[k].abs().max()) < 6 for k in ("b", "h0", "dh", "dlast"))
+    extra = (2.0 ** -1009 if kind == torch.float64 else 2.0 ** -124) * 2.0 ** 31
+    za, zb, zh0 = ref.host(x["a"]), ref.host(x["b"]), ref.host(x["h0"])
+    h, last = sla.sla_recur_solve(x["a"], x["b"], x["h0"], x["off"], gate=gate)
+    want, wlast, e, elast = ref.solve(za, zb, zh0, x["offsets"], gate, kind)
+    ref.within(h, want, ref.storage(want, e + extra, kind))
+    ref.within(last, wlast, ref.storage(wlast, elast + extra, ref.wide(kind)))
+    got = sla.sla_recur_adjoint(x["a"], h, x["dh"], b=x["b"], h0=x["h0"], seq_off=x["off"], dh_last=x["dlast"], gate=gate)
+    want = ref.adjoint(za, zb, ref.host(h), zh0, ref.host(x["dh"]), ref.host(x["dlast"]), x["offsets"], gate, kind)
+    for name, t in zip(("da", "db", "dh0"), got):
+        v, e = want[name]
+        ref.within(t, v, ref.storage(v, e + extra, ref.wide(kind) if name == "dh0" else kind))
+    state = x["h0"][:1].expand(7, d).contiguous()          # and the single step
+    h = sla.sla_recur_step(x["a"][:7], x["b"][:7], state, gate=gate)
+    for r in range(7):
+        w, _, e, _ = ref.solve(za[r:r + 1], zb[r:r + 1], zh0[:1], [0, 1], gate, kind)
+        ref.within(h[r:r + 1], w, ref.storage(w, e + extra, kind))
+
+
 def test_slow_decay_keeps_far_inputs():
     """Coefficients of 1 sum: an input reaches every later row through all chunks."""
     tokens, d = 5000, 40
