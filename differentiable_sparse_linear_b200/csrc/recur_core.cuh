@@ -192,11 +192,11 @@ __device__ __forceinline__ B apply(A a, B x, B h)
 {
     return (is_const(a) || x == B(0)) ? h : fma_of(B(a), x, h);
 }
-// The product of a later a2 and an earlier a1.
+// The product of a later a2 and an earlier a1.  Rounded before 0 is added: a negative one that vanishes is no mark.
 template <typename A>
 __device__ __forceinline__ A product(A a2, A a1)
 {
-    return (is_const(a1) || is_const(a2)) ? const_mark<A>() : a2 * a1 + A(0);
+    return (is_const(a1) || is_const(a2)) ? const_mark<A>() : add_of(mul_of(a2, a1), A(0));
 }
 // apply() with an A wider than fp32's range (published maps): the fp64 product, rounded once with the sum
 __device__ __forceinline__ float apply_wide(double a, float x, float h)
@@ -240,16 +240,18 @@ struct Words<float> {
     static __device__ __forceinline__ bool fixed(unsigned a) { return a == CONST; }
     unsigned long long w[1];
     // A as it is published: every user of the map, its own chunk included, applies this one.  An A within fp32's
-    // range is converted by shifts (subnormal ones are 0), an overflowed one is `wide`.
+    // range is converted by shifts (subnormal ones are +0, so that no state is cut off), an overflowed one is `wide`.
     static __device__ __forceinline__ unsigned pack(float a)
     {
         const unsigned b = __float_as_uint(a), mag = b & 0x7fffffffu;
-        return (b & 0x80000000u) | (mag < 0x00800000u ? 0u : ((mag + 4u) >> 3) + (896u << 20));
+        return mag >= 0x00800000u ? (b & 0x80000000u) | (((mag + 4u) >> 3) + (896u << 20)) : mag ? 0u : b;
     }
     static __device__ __forceinline__ unsigned pack(double a)
     {
         if (!(a == a))
             return 0x7ff80000u;
+        if (fabs(a) < 1e-300)
+            return is_const(a) ? CONST : 0u;
         return (unsigned)(((unsigned long long)__double_as_longlong(a) + 0x80000000ull) >> 32);
     }
     static __device__ __forceinline__ float apply(unsigned a, float x, float h)
@@ -912,23 +914,24 @@ struct Recur {
             }
         }
     }
-    // Every run gets the map of the runs in front of it.  CUT: behind a constant map all are.
+    // Every run gets the map of the runs in front of it.  CUT: behind a constant map all are; a product that vanishes
+    // is +0, no mark.
     template <bool CUT>
     __device__ __forceinline__ void front_maps(int buf, int place, Runs &q)
     {
         A fa = A(1), fh = A(0);
+        bool cut = false;
         for (int r0 = 0; r0 < P::NR; r0 += HELD) {
             if (HELD < P::NR)
                 take(buf, place, r0, q);
 #pragma unroll
             for (int k = 0; k < HELD; ++k) {
-                sm.mapA[buf][r0 + k][place] = fa;
+                sm.mapA[buf][r0 + k][place] = CUT && cut ? const_mark<A>() : add_of(fa, A(0));
                 sm.mapH[buf][r0 + k][place] = fh;
                 fh = fma_of(q.a[k], fh, q.h[k]);
-                if (CUT && (is_const(fa) || is_const(q.a[k])))
-                    fa = const_mark<A>();
-                else
-                    fa = fma_of(fa, q.a[k], A(0));         // -0 marks a constant map
+                if (CUT)
+                    cut = cut || is_const(q.a[k]);
+                fa = mul_of(fa, q.a[k]);
             }
         }
     }
@@ -996,7 +999,7 @@ struct Recur {
         if (HELD == P::NR)
             take(buf, place, 0, q);
         tile_map(buf, place, q, ta, th);
-        typename Wd::Map pa = Wd::pack(pl.cut ? const_mark<A>() : ta + A(0));
+        typename Wd::Map pa = Wd::pack(pl.cut ? const_mark<A>() : add_of(ta, A(0)));
         int how = pl.cut ? 2 : 1;
         if (!(isfinite(ta) && isfinite(th))) {
             double wa;

@@ -240,6 +240,33 @@ def test_not_finite_stays_in_its_channel_and_sequence():
     assert torch.equal(db[keep], clean[keep])
 
 
+@pytest.mark.parametrize("kind", ref.KINDS)
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("low", [0.3, 0.45])
+def test_not_finite_states_stay_over_vanishing_products(kind, value, low):
+    """Products of coefficients that leave the range, of either sign, over a few hundred rows: a state that is not
+    finite stays so to the end of its sequence, and does not reach the next one."""
+    kind = ref.KINDS[kind]
+    g = torch.Generator().manual_seed(5)
+    tokens, d, border = 2500, 96, 2100
+    a = low + (0.9 - low) * torch.rand(tokens, d, generator=g)
+    a[torch.rand(tokens, d, generator=g) < 0.5] *= -1
+    a = a.to(kind).cuda()
+    x = torch.randn(tokens, d, generator=g).to(kind).cuda()
+    off = torch.tensor([0, border, tokens], dtype=torch.int32).cuda()
+    h0 = torch.zeros(2, d, dtype=ref.wide(kind), device="cuda")
+    b = x.clone()
+    b[10] = value
+    h, last = sla.sla_recur_solve(a, b, h0, off)
+    assert h[:10].isfinite().all() and not h[10:border].isfinite().any() and h[border:].isfinite().all()
+    assert not last[0].isfinite().any() and last[1].isfinite().all()
+    dh = x.clone()
+    dh[border - 10] = value
+    _, db, dh0 = sla.sla_recur_adjoint(a, x, dh, h0=h0, seq_off=off)
+    assert not db[:border - 9].isfinite().any() and db[border - 9:].isfinite().all()
+    assert not dh0[0].isfinite().any() and dh0[1].isfinite().all()
+
+
 def test_partial_gradients():
     x = data("ragged", 56, torch.bfloat16, "sigmoid")
     h, _ = sla.sla_recur_solve(x["a"], x["b"], x["h0"], x["off"], gate="sigmoid")
