@@ -391,7 +391,10 @@ SLA_API size_t sla_recur_workspace_bytes(int32_t dtype, int64_t n_tokens, int64_
 /* h_t = a_t h_{t-1} + w_t b_t over every sequence, from d_h0 (n_seq x n_chan, fp32 or fp64;
  * NULL: zero states).  d_h gets
  * the rows; d_h_last (n_seq x n_chan, fp32/fp64, may be NULL) the unrounded last states (an empty
- * sequence's is its first one).  flags: 0 or SLA_FILL_REST. */
+ * sequence's is its first one).  flags: 0 or SLA_FILL_REST.  A state that is not finite is not to
+ * the end of its sequence (it may turn from infinite to NaN), and reaches no other channel or
+ * sequence; a coefficient that is not finite is used only where the state in front of it is not 0,
+ * or not at all (a run of coefficients may overflow over rows that are 0). */
 SLA_API sla_status sla_recur_solve(int32_t dtype, int32_t gate, int64_t n_tokens, int64_t n_chan,
                                    int32_t n_seq, const int32_t *d_seq_off, const void *d_a,
                                    int64_t lda, const void *d_b, int64_t ldb, const void *d_h0,
