@@ -43,7 +43,7 @@
 // one another's results once a tile and for fixed latencies in between; 16 warps of 128 registers are all that fit.
 // Measured on the way (solve 65536 x 4096 bf16): every gate twice instead of kept coefficients and combining runs by
 // shuffles 655 us, maps by the scan warps 532, four scan threads a channel 501, tensor copies, kept coefficients and
-// paired arithmetic 455, first states as entering states 424, guards out of line 403.  Rows of 128 bytes by a bulk copy
+// paired arithmetic 455, first states as entering states 424, guards out of line 403 to 414.  Rows of 128 bytes by a bulk copy
 // each took 185 us where tensor copies take 105 (16384 x 4096); copies by one warp's cp.async 171; runs of 8 rows by 7 warps 157; two blocks of half a
 // tile an SM 215.  Few channels leave few chunks side by side and the chain of chunks bounds: 200000 x 64 bf16 takes
 // 106 us of a floor of 12.  Tiles with borders cost half as much again (16384 x 4096 in 100 sequences: 161 us).
