@@ -36,17 +36,18 @@
 // tickets only, whose blocks are running, so the wait ends however many blocks are resident; it
 // is bounded all the same, and a chunk that gave up goes on with NaN.
 //
-// What bounds it.  Memory must carry z, b and h once (backward z, g, h, dz, db): 6 (10) bytes a value in 16 bits.  The
-// kernel moves little more (380 of 403 MB at 16384 x 4096 bf16, forward, besides 8 + 4 bytes a channel and chunk
-// of published words) but runs at 0.55 to 0.6 of the copy rate there, 105 us, 0.66 in fp32 (16384 x 2048, 93 us),
-// backward 0.6 (170 us) and 0.79 (130 us): about 23 instructions a value at 39 % of the issue slots.  Warps wait for
-// one another's results once a tile and for fixed latencies in between; 16 warps of 128 registers are all that fit.
-// Measured on the way (solve 65536 x 4096 bf16): every gate twice instead of kept coefficients and combining runs by
-// shuffles 655 us, maps by the scan warps 532, four scan threads a channel 501, tensor copies, kept coefficients and
-// paired arithmetic 455, first states as entering states 424, guards out of line 403 to 414.  Rows of 128 bytes by a bulk copy
-// each took 185 us where tensor copies take 105 (16384 x 4096); copies by one warp's cp.async 171; runs of 8 rows by 7 warps 157; two blocks of half a
-// tile an SM 215.  Few channels leave few chunks side by side and the chain of chunks bounds: 200000 x 64 bf16 takes
-// 106 us of a floor of 12.  Tiles with borders cost half as much again (16384 x 4096 in 100 sequences: 161 us).
+// What bounds it.  Memory must carry z, b and h once (backward z, g, h, dz, db): 6 (10) bytes a value in 16
+// bits.  The kernel moves little more (380 of 403 MB at 16384 x 4096 bf16, forward, besides 8 + 4 bytes a channel
+// and chunk of published words) but runs at 0.55 to 0.6 of the copy rate there, 105 us, 0.66 in fp32 (16384 x
+// 2048, 93 us), backward 0.6 (170 us) and 0.79 (130 us): about 23 instructions a value at 39 % of the issue
+// slots.  Warps wait for one another's results once a tile and for fixed latencies in between; 16 warps of 128
+// registers are all that fit. Measured on the way (solve 65536 x 4096 bf16): every gate twice instead of kept
+// coefficients and combining runs by shuffles 655 us, maps by the scan warps 532, four scan threads a channel 501,
+// tensor copies, kept coefficients and paired arithmetic 455, first states as entering states 424, guards out of
+// line 403 to 414.  Rows of 128 bytes by a bulk copy each took 185 us where tensor copies take 105 (16384 x 4096);
+// copies by one warp's cp.async 171; runs of 8 rows by 7 warps 157; two blocks of half a tile an SM 215.  Few
+// channels leave few chunks side by side and the chain of chunks bounds: 200000 x 64 bf16 takes 106 us of a floor
+// of 12.  Tiles with borders cost half as much again (16384 x 4096 in 100 sequences: 161 us).
 //
 // A sequence border inside a run makes its map constant.  Such a map is marked by A = -0 (products are
 // normalised to +0), because 0 * x would carry a NaN or an infinity across the border.  Where the entering state is
