@@ -798,6 +798,7 @@ struct Recur {
                     }
                 }
             }
+            __syncwarp();                                  // the copies of a later tile into these rows are other lanes'
         }
     }
 
