@@ -50,9 +50,11 @@
 // of 12.  Tiles with borders cost half as much again (16384 x 4096 in 100 sequences: 161 us).
 //
 // A sequence border inside a run makes its map constant.  Such a map is marked by A = -0 (products are
-// normalised to +0), because 0 * x would carry a NaN or an infinity across the border.  Where the entering state is
-// exactly 0, A is not used, so that a product of large coefficients that overflowed does no harm to rows
-// of zeros.
+// normalised to +0), because 0 * x would carry a NaN or an infinity across the border.
+//
+// A channel whose (A, H) is not finite has no map: a coefficient or an input is not, or a product or a sum of the
+// tile left the range, although the states themselves may stay in it.  Its rows are read again and taken one
+// by one from the state that enters the tile, and later chunks wait for the one that leaves.
 #pragma once
 
 #include <cuda.h>
@@ -187,24 +189,12 @@ __device__ __forceinline__ bool is_const(float a) { return __float_as_uint(a) ==
 __device__ __forceinline__ bool is_const(double a) { return (unsigned long long)__double_as_longlong(a) == 0x8000000000000000ull; }
 template <typename A>
 __device__ __forceinline__ A const_mark() { return A(-0.0); }
-// x -> A x + H at x; at x = 0 without A, which may have overflowed.
-template <typename A, typename B>
-__device__ __forceinline__ B apply(A a, B x, B h)
-{
-    return (is_const(a) || x == B(0)) ? h : fma_of(B(a), x, h);
-}
-// The product of a later a2 and an earlier a1.  Rounded before 0 is added: a negative one that vanishes is no mark.
+// x -> A x + H at x
 template <typename A>
-__device__ __forceinline__ A product(A a2, A a1)
+__device__ __forceinline__ A apply(A a, A x, A h)
 {
-    return (is_const(a1) || is_const(a2)) ? const_mark<A>() : add_of(mul_of(a2, a1), A(0));
+    return is_const(a) ? h : fma_of(a, x, h);
 }
-// apply() with an A wider than fp32's range (published maps): the fp64 product, rounded once with the sum
-__device__ __forceinline__ float apply_wide(double a, float x, float h)
-{
-    return (is_const(a) || x == 0.0f) ? h : (float)__fma_rn(a, (double)x, (double)h);
-}
-__device__ __forceinline__ double apply_wide(double a, double x, double h) { return apply(a, x, h); }
 
 // ------------------------------------------------------------------ published words
 __device__ __forceinline__ unsigned long long ld_word(const unsigned long long *p)
@@ -240,26 +230,18 @@ struct Words<float> {
     static constexpr unsigned CONST = 0x80000000u;         // packed A of a constant map
     static __device__ __forceinline__ bool fixed(unsigned a) { return a == CONST; }
     unsigned long long w[1];
-    // A as it is published: every user of the map, its own chunk included, applies this one.  An A within fp32's
-    // range is converted by shifts (subnormal ones are +0, so that no state is cut off), an overflowed one is `wide`.
+    // A as it is published: every user of the map, its own chunk included, applies this one.  Converted by shifts
+    // (subnormal ones are +0, so that no state is cut off).
     static __device__ __forceinline__ unsigned pack(float a)
     {
         const unsigned b = __float_as_uint(a), mag = b & 0x7fffffffu;
         return mag >= 0x00800000u ? (b & 0x80000000u) | (((mag + 4u) >> 3) + (896u << 20)) : mag ? 0u : b;
     }
-    static __device__ __forceinline__ unsigned pack(double a)
-    {
-        if (!(a == a))
-            return 0x7ff80000u;
-        if (fabs(a) < 1e-300)
-            return is_const(a) ? CONST : 0u;
-        return (unsigned)(((unsigned long long)__double_as_longlong(a) + 0x80000000ull) >> 32);
-    }
     static __device__ __forceinline__ float apply(unsigned a, float x, float h)
     {
         const unsigned mag = a & 0x7fffffffu;
-        if (mag >= ((1023u + 127u) << 20))                 // beyond fp32, and NaN
-            return apply_wide(__hiloint2double((int)a, 0), x, h);
+        if (fixed(a))
+            return h;
         const unsigned f = mag < (897u << 20) ? 0u : (mag - (896u << 20)) << 3;
         return __fmaf_rn(__uint_as_float((a & 0x80000000u) | f), x, h);
     }
@@ -287,7 +269,7 @@ struct Words<double> {
         return x == x ? (unsigned long long)__double_as_longlong(x) : QUIET;
     }
     static __device__ __forceinline__ double pack(double a) { return a; }
-    static __device__ __forceinline__ double apply(double a, double x, double h) { return apply_wide(a, x, h); }
+    static __device__ __forceinline__ double apply(double a, double x, double h) { return sla::apply(a, x, h); }
     static __device__ __forceinline__ void put(unsigned long long *p, double a, double h)
     {
         st_word(p, bits(a));
@@ -898,8 +880,8 @@ struct Recur {
             q.h[k] = sm.mapH[buf][r0 + k][place];
         }
     }
-    // The tile's (A, H) in A's own type, a constant map's -0 as the factor 0 that it is.  That is right as long as
-    // everything is finite, and leaves a result that is not where it is not (infinity times 0).
+    // The tile's (A, H), a constant map's -0 as the factor 0 that it is.  That is right as long as everything is finite, and
+    // leaves a result that is not where it is not (infinity times 0).
     __device__ __forceinline__ void tile_map(int buf, int place, Runs &q, A &ta, A &th) const
     {
         ta = A(1);
@@ -937,60 +919,84 @@ struct Recur {
             }
         }
     }
-    // Both again where the tile's result is not finite, with constant maps and zero states looked at and the product in
-    // fp64 (of four runs each, 16 coefficients); rare, and out of the way of the others' code.  `fit`: the
-    // front maps' products stay in A's range.
-    static __device__ __noinline__ void guarded_map(const Sm &sm, int buf, int place, double &wa, A &th, bool &fit)
+    // The leaving state of a tile with borders, with constant maps looked at: what lies in front of the last one does not
+    // count, finite or not.
+    static __device__ __noinline__ A last_state(const Sm &sm, int buf, int place)
     {
-        wa = 1.0;
-        th = A(0);
-        A fa = A(1);
-        fit = true;
-#pragma unroll 1
-        for (int r = 0; r < P::NR; r += 4) {
-            A m = A(1);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const A a = sm.mapA[buf][r + e][place];
-                th = apply(a, th, sm.mapH[buf][r + e][place]);
-                m = product(a, m);
-                fa = product(a, fa);
-                fit = fit && !isinf(fa);
-            }
-            wa = product((double)m, wa);
-        }
+        A h = A(0);
+#pragma unroll 4
+        for (int r = 0; r < P::NR; ++r)
+            h = apply(sm.mapA[buf][r][place], h, sm.mapH[buf][r][place]);
+        return h;
     }
-    static __device__ __noinline__ void guarded_fronts(Sm &sm, int buf, int place)
+    // A channel of a tile row by row, as pass 2 takes it, from the state x that enters it: where no finite map says what
+    // the tile does (a coefficient or an input that is not finite, or a product or sum beyond A's range).  The rows are
+    // read from memory again, 16 (fp64: 8) at a time; rare, and out of the way of the others' code.  Returns the
+    // state that leaves.  `own`: that it does not depend on x (behind a border or a row outside), or is not finite
+    // whatever x is.
+    // FRONTS: every run gets the constant map of the state that enters it, which comes from the runs' maps up to the
+    // first that is not finite, and again behind a border: those rows keep the bits that they have without it.
+    template <bool FRONTS>
+    static __device__ __noinline__ A walk(const RecurArgs<S> &g, Sm &sm, int slot, int buf, int place, A x, bool &own)
     {
+        constexpr int N = 64 / (int)sizeof(A);
+        static_assert(C % N == 0 && N % R == 0, "whole runs");
+        const TilePlan pl = sm.plan[slot];
+        const int64_t ch = (int64_t)pl.cb * P::W + chan_at(place);
+        const A x0 = x;
         A fa = A(1), fh = A(0);
+        bool mapped = FRONTS;
+        own = false;
 #pragma unroll 1
-        for (int r = 0; r < P::NR; ++r) {
-            const A a = sm.mapA[buf][r][place], h = sm.mapH[buf][r][place];
-            sm.mapA[buf][r][place] = fa;
-            sm.mapH[buf][r][place] = fh;
-            fh = apply(a, fh, h);
-            fa = product(a, fa);
-        }
-    }
-    // Every run gets the constant map of the state that enters it, from x, run by run: where products of
-    // coefficients leave A's range.
-    static __device__ __noinline__ void front_states(Sm &sm, int buf, int place, A x)
-    {
-#pragma unroll 1
-        for (int r0 = 0; r0 < P::NR; r0 += 4) {
-            A a[4], h[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                a[k] = sm.mapA[buf][r0 + k][place];
-                h[k] = sm.mapH[buf][r0 + k][place];
+        for (int p0 = 0; p0 < C; p0 += N) {
+            if (!pl.seg && isnan(x)) {                     // it stays so: no row is needed
+                for (int r = p0 / R; FRONTS && r < P::NR; ++r) {
+                    sm.mapA[buf][r][place] = const_mark<A>();
+                    sm.mapH[buf][r][place] = x;
+                }
+                return x;
             }
+            A z[N], u[N];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                sm.mapA[buf][r0 + k][place] = const_mark<A>();
-                sm.mapH[buf][r0 + k][place] = x;
-                x = apply(a[k], x, h[k]);
+            for (int i = 0; i < N; ++i) {
+                const int64_t pos = (int64_t)pl.chunk * C + p0 + i, t = REV ? g.q.n_tokens - 1 - pos : pos;
+                const bool inside = p0 + i >= pl.lo && p0 + i < pl.hi;
+                z[i] = inside ? RT::up(g.in[0][t * g.ldin[0] + ch]) : A(0);
+                u[i] = inside && (!REV || g.in[1]) ? RT::up(g.in[1][t * g.ldin[1] + ch]) : A(0);
+            }
+            A a[N], w[N];
+            gates_of<GATE, sizeof(S) == 2>(z, a, w);
+            if constexpr (!REV && GATE == SLA_GATE_SIGMOID)
+                vmul(u, w, u);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int p = p0 + i;
+                if (FRONTS && i % R == 0) {
+                    A &ra = sm.mapA[buf][p / R][place], &rh = sm.mapH[buf][p / R][place];
+                    const A qa = ra, qh = rh;
+                    if (mapped)
+                        x = apply(fa, x0, fh);
+                    ra = const_mark<A>();
+                    rh = x;
+                    fh = apply(qa, fh, qh);
+                    fa = is_const(qa) || is_const(fa) ? const_mark<A>() : add_of(mul_of(fa, qa), A(0));
+                    mapped = (mapped || is_const(qa)) && isfinite(fa) && isfinite(fh);
+                }
+                if (p < pl.lo || p >= pl.hi) {
+                    x = A(0);
+                    own = true;
+                    continue;
+                }
+                const int s = pl.seg ? sm.begin[slot][p] : -1;
+                if (s >= 0) {
+                    x = g.enter ? g.enter[(int64_t)s * g.n_chan + ch] : A(0);
+                    own = true;
+                }
+                x = REV ? mul_of(a[i], add_of(u[i], x)) : fma_of(a[i], x, u[i]);
+                own = own || !isfinite(u[i]) || isnan(a[i]);
             }
         }
+        return mapped ? apply(fa, x0, fh) : x;
     }
     // one channel of a tile: its map, published
     __device__ __forceinline__ void maps(const TilePlan &pl, int buf, int place, Runs &q)
@@ -1003,12 +1009,12 @@ struct Recur {
         tile_map(buf, place, q, ta, th);
         typename Wd::Map pa = Wd::pack(pl.cut ? const_mark<A>() : add_of(ta, A(0)));
         int how = pl.cut ? 2 : 1;
-        if (!(isfinite(ta) && isfinite(th))) {
-            double wa;
-            bool fit;
-            guarded_map(sm, buf, place, wa, th, fit);
-            pa = Wd::pack(wa);
-            how = fit ? 3 : 0;                             // 0: a state warp goes through the runs
+        if (!(isfinite(ta) && isfinite(th)) && ch < g.n_chan) {
+            how = 0;                                       // there is no map, a state warp goes through the rows
+            if (pl.cut)
+                th = last_state(sm, buf, place);
+            if (!(pl.cut && isfinite(th)))
+                pa = Wd::pack(A(0));
         }
         sm.fronts[buf][place] = (unsigned char)how;
         sm.tileA[buf][place] = pa;
@@ -1017,9 +1023,21 @@ struct Recur {
             const int64_t cell = (int64_t)pl.chunk * g.n_chan + ch;
             if (Wd::fixed(pa))
                 st_word((typename Wd::Inc *)g.inc + cell, Wd::inc_bits(th));
-            else if (enters(pl))
+            else if (how && enters(pl))
                 Wd::put(g.agg + cell * Wd::N, pa, th);
         }
+    }
+    // One channel without a map: a leaving state that does not depend on the entering one is published without waiting for
+    // that, so that tiles full of NaN do not wait for one another.
+    __device__ __forceinline__ void own_state(const TilePlan &pl, int slot, int buf, int place)
+    {
+        using Wd = Words<A>;
+        if (Wd::fixed(sm.tileA[buf][place]))                   // it is published
+            return;
+        bool own;
+        const A x = walk<false>(g, sm, slot, buf, place, A(0), own);
+        if (own && pl.chunk + 1 < g.n_chunks)
+            st_word((typename Wd::Inc *)g.inc + (int64_t)pl.chunk * g.n_chan + (int64_t)pl.cb * P::W + chan_at(place), Wd::inc_bits(x));
     }
 
     // whether the tile's own state depends on the chunks before it: not where a border (or a row outside) is at its
@@ -1049,8 +1067,8 @@ struct Recur {
             return state_before<A, 8>(pl.chunk, g.n_chan, ch, g.agg, inc);
         return state_before<A, 16 / Words<A>::N>(pl.chunk, g.n_chan, ch, g.agg, inc);
     }
-    // its leaving state, published, and where the maps do not compose the runs' states
-    __device__ __forceinline__ void hand_over(const TilePlan &pl, int buf, int place, A x)
+    // its leaving state, published, and where there is no map the states that enter the runs
+    __device__ __forceinline__ void hand_over(const TilePlan &pl, int slot, int buf, int place, A x)
     {
         using Wd = Words<A>;
         const int64_t ch = (int64_t)pl.cb * P::W + chan_at(place);
@@ -1059,10 +1077,10 @@ struct Recur {
         sm.enter[buf][place] = x;
         if (ch >= g.n_chan)
             return;
-        if (pl.chunk + 1 < g.n_chunks && !Wd::fixed(pa))
-            st_word((typename Wd::Inc *)g.inc + (int64_t)pl.chunk * g.n_chan + ch, Wd::inc_bits(Wd::apply(pa, x, th)));
-        if (!sm.fronts[buf][place])
-            front_states(sm, buf, place, x);
+        bool own = Wd::fixed(pa);                              // published by the map warp
+        x = sm.fronts[buf][place] ? Wd::apply(pa, x, th) : walk<true>(g, sm, slot, buf, place, x, own);
+        if (pl.chunk + 1 < g.n_chunks && !own)
+            st_word((typename Wd::Inc *)g.inc + (int64_t)pl.chunk * g.n_chan + ch, Wd::inc_bits(x));
     }
 
     // What the plan warp keeps from tile to tile: the ticket drawn ahead, the first and last row of all sequences, and
@@ -1272,8 +1290,8 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
                     r.template front_maps<false>(odd, place, q);
                 else if (how == 2)
                     r.template front_maps<true>(odd, place, q);
-                else if (how == 3)
-                    K::guarded_fronts(sm, odd, place);
+                else
+                    r.own_state(pl, slot, odd, place);
             }
             __syncwarp();
             bar_arrive(BAR_ENTER + odd, ENTER);
@@ -1292,7 +1310,7 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
             __syncwarp();
             bar_sync(BAR_TILE + odd, TILE);
             if (place < P::W)
-                r.hand_over(pl, odd, place, x);
+                r.hand_over(pl, slot, odd, place, x);
             __syncwarp();
             bar_arrive(BAR_ENTER + odd, ENTER);
         }

@@ -393,8 +393,10 @@ SLA_API size_t sla_recur_workspace_bytes(int32_t dtype, int64_t n_tokens, int64_
  * the rows; d_h_last (n_seq x n_chan, fp32/fp64, may be NULL) the unrounded last states (an empty
  * sequence's is its first one).  flags: 0 or SLA_FILL_REST.  A state that is not finite is not to
  * the end of its sequence (it may turn from infinite to NaN), and reaches no other channel or
- * sequence; a coefficient that is not finite is used only where the state in front of it is not 0,
- * or not at all (a run of coefficients may overflow over rows that are 0). */
+ * sequence.  A coefficient that is not finite makes it so whatever the state in front of it, 0 and a
+ * sequence's missing first state included (0 times it is NaN).  Finite coefficients over several
+ * rows may have a product beyond the range where the states stay inside: the result is that of one
+ * row after the other, but such rows are slow. */
 SLA_API sla_status sla_recur_solve(int32_t dtype, int32_t gate, int64_t n_tokens, int64_t n_chan,
                                    int32_t n_seq, const int32_t *d_seq_off, const void *d_a,
                                    int64_t lda, const void *d_b, int64_t ldb, const void *d_h0,
