@@ -54,7 +54,8 @@
 //
 // A channel whose (A, H) is not finite has no map: a coefficient or an input is not, or a product or a sum of the
 // tile left the range, although the states themselves may stay in it.  Its rows are read again and taken one
-// by one from the state that enters the tile, and later chunks wait for the one that leaves.
+// by one from the state that enters the tile, and later chunks wait for the one that leaves.  A product that
+// vanishes counts as 0.
 #pragma once
 
 #include <cuda.h>
@@ -881,7 +882,8 @@ struct Recur {
         }
     }
     // The tile's (A, H), a constant map's -0 as the factor 0 that it is.  That is right as long as everything is finite, and
-    // leaves a result that is not where it is not (infinity times 0).
+    // leaves a result that is not where it is not (infinity times 0): in the order of front_maps(), so that (A, H) is
+    // finite only where the maps of all the runs in front are.
     __device__ __forceinline__ void tile_map(int buf, int place, Runs &q, A &ta, A &th) const
     {
         ta = A(1);
@@ -890,11 +892,9 @@ struct Recur {
             if (HELD < P::NR)
                 take(buf, place, r0, q);
 #pragma unroll
-            for (int k = 0; k < HELD; k += 4) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    th = fma_of(q.a[k + e], th, q.h[k + e]);
-                ta *= (q.a[k] * q.a[k + 1]) * (q.a[k + 2] * q.a[k + 3]);
+            for (int k = 0; k < HELD; ++k) {
+                th = fma_of(q.a[k], th, q.h[k]);
+                ta = mul_of(ta, q.a[k]);
             }
         }
     }

@@ -396,7 +396,10 @@ SLA_API size_t sla_recur_workspace_bytes(int32_t dtype, int64_t n_tokens, int64_
  * sequence.  A coefficient that is not finite makes it so whatever the state in front of it, 0 and a
  * sequence's missing first state included (0 times it is NaN).  Finite coefficients over several
  * rows may have a product beyond the range where the states stay inside: the result is that of one
- * row after the other, but such rows are slow. */
+ * row after the other, but such rows are slow.  A product of coefficients of consecutive rows below
+ * 2^-126 (fp64: 2^-1022) in magnitude may count as 0: what is left of the state in front of them is
+ * lost then, also where later coefficients above 1 would bring it back.  The adjoint's lambda has
+ * the same limits. */
 SLA_API sla_status sla_recur_solve(int32_t dtype, int32_t gate, int64_t n_tokens, int64_t n_chan,
                                    int32_t n_seq, const int32_t *d_seq_off, const void *d_a,
                                    int64_t lda, const void *d_b, int64_t ldb, const void *d_h0,

@@ -81,3 +81,65 @@ def test_coefficients_that_are_not_finite(gate, kind, first):
         mask = torch.cat([torch.isfinite(t[s:s + n]) for t in (h, back[0], back[1])])
         masks = mask if masks is None else masks
         assert torch.equal(mask, masks)
+
+
+def overshoots(kind):
+    """({row: exponent of a}, {row: exponent of b}, exponent of the first state, sign) of columns whose states stay in
+    range while products of coefficients, or sums from a zero state, overflow.  Powers of two: every state is exact.
+    No two neighbouring coefficients have a product below 2^-126 (fp64 2^-1022), which may count as 0."""
+    s = 8 if kind == torch.float64 else 1
+    top = 1023 if s == 8 else 127
+    out = []
+    for p in (0, 1, 3, 5, 100, 160, 172, 175, 176, 177, 300):
+        for sign in (1, -1):
+            for a, first in (({p: 50, p + 4: 50, p + 16: 66, p + 20: -66}, -100), ({p + 12: 100, p + 16: 66, p + 20: -66}, -83),
+                             ({p: 100, p + 1: 100, p + 2: -50, p + 3: -50}, -80), ({p: 70, p + 176: 70, p + 352: -70}, -100),
+                             ({p: 100, p + 40: 100}, -120), ({p: 100, p + 3: 60, p + 9: 60, p + 90: -60}, -120)):
+                out.append(({r: e * s for r, e in a.items()}, {}, first * s, sign))
+        out.append(({}, {p: top, p + 50: top}, top, 0))       # -2^top, then 0, then 2^top
+    return out
+
+
+@pytest.mark.parametrize("kind", ["f32", "f64", "bf16"])
+@pytest.mark.parametrize("off", [[0, 800], [3, 783], [0, 200, 200, 790], [0, 5, 170, 185, 800]])
+def test_products_beyond_the_range(kind, off):
+    """The states are those of the rows one after the other, bit for bit: backward the same columns, reversed."""
+    kind = ref.KINDS[kind]
+    cases, n = overshoots(kind), len(off) - 1
+    T, d = 800, len(cases)
+    a, b, first = np.ones((T, d)), np.zeros((T, d)), np.zeros((n, d))
+    for c, (ea, eb, e0, sign) in enumerate(cases):
+        for s in range(n):                                 # in every sequence, from its first row on
+            for r, e in ea.items():
+                if off[s] + r < off[s + 1]:
+                    a[off[s] + r, c] = (sign if r % 4 == 0 else 1) * 2.0 ** e
+            for r, e in eb.items():
+                if off[s] + r < off[s + 1]:
+                    b[off[s] + r, c] = 2.0 ** e
+            first[s, c] = -2.0 ** e0 if sign == 0 else 2.0 ** e0
+    put = lambda x, k: torch.from_numpy(x).to(k).cuda()  # noqa: E731
+    o = torch.tensor(off, dtype=torch.int32).cuda()
+    want, wlast = by_rows(a, b, first, off, "value")
+    assert np.isfinite(want).all() and np.abs(want).max() < torch.finfo(kind).max
+    for pad in (0, 1):                                     # aligned rows and others
+        A, B = (torch.nn.functional.pad(put(x, kind), (0, pad)) for x in (a, b))
+        h, last = sla.sla_recur_solve(A[:, :d], B[:, :d], put(first, ref.wide(kind)), o)
+        assert np.array_equal(ref.host(h), want) and np.array_equal(ref.host(last), wlast)
+        # lambda_t = g_t + a_{t+1} lambda_{t+1}: with a and b turned round, the last state is dL/dh_last and the
+        # states (before the coefficient) are those of the reversed rows
+        ra, rb, roff = a[::-1].copy(), b[::-1].copy(), [T - v for v in off[::-1]]
+        lam, dh0 = np.zeros((T, d)), np.zeros((n, d))
+        for s in range(n):
+            v = first[::-1][s]
+            for t in range(roff[s + 1] - 1, roff[s] - 1, -1):
+                lam[t] = rb[t] + v
+                v = ra[t] * lam[t]
+            dh0[s] = v
+        ro = torch.tensor(roff, dtype=torch.int32).cuda()
+        RA, RB = (torch.nn.functional.pad(put(x, kind), (0, pad)) for x in (ra, rb))
+        ok = np.isfinite(lam).all(0) & (np.abs(lam) < torch.finfo(kind).max).all(0) & (np.abs(dh0) < torch.finfo(kind).max).all(0)
+        assert ok.sum() > d // 2
+        da, db, got0 = sla.sla_recur_adjoint(RA[:, :d], torch.zeros_like(RA)[:, :d], RB[:, :d], h0=torch.zeros_like(put(first, ref.wide(kind))),
+                                             seq_off=ro, dh_last=put(first[::-1].copy(), ref.wide(kind)))
+        assert np.array_equal(ref.host(db)[:, ok], lam[:, ok]) and np.array_equal(ref.host(got0)[:, ok], dh0[:, ok])
+        assert (ref.host(da)[:, ok] == 0).all()
