@@ -219,40 +219,25 @@ __device__ __forceinline__ void st_word(unsigned *p, unsigned v)
     asm volatile("st.relaxed.gpu.global.b32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// fp32 arithmetic: one word of A's upper 32 bits as fp64 (its range; 2^-21 relative, once per chunk) and H.
-// fp64: a word each.
+// fp32 arithmetic: one word of A and H.  fp64: a word each.  Only finite maps are published, so no word of theirs has all
+// bits set.
 template <typename A>
 struct Words;
 template <>
 struct Words<float> {
     static constexpr int N = 1;
     using Inc = unsigned;
-    using Map = unsigned;
-    static constexpr unsigned CONST = 0x80000000u;         // packed A of a constant map
-    static __device__ __forceinline__ bool fixed(unsigned a) { return a == CONST; }
     unsigned long long w[1];
-    // A as it is published: every user of the map, its own chunk included, applies this one.  Converted by shifts
-    // (subnormal ones are +0, so that no state is cut off).
-    static __device__ __forceinline__ unsigned pack(float a)
+    static __device__ __forceinline__ void put(unsigned long long *p, float a, float h)
     {
-        const unsigned b = __float_as_uint(a), mag = b & 0x7fffffffu;
-        return mag >= 0x00800000u ? (b & 0x80000000u) | (((mag + 4u) >> 3) + (896u << 20)) : mag ? 0u : b;
-    }
-    static __device__ __forceinline__ float apply(unsigned a, float x, float h)
-    {
-        const unsigned mag = a & 0x7fffffffu;
-        if (fixed(a))
-            return h;
-        const unsigned f = mag < (897u << 20) ? 0u : (mag - (896u << 20)) << 3;
-        return __fmaf_rn(__uint_as_float((a & 0x80000000u) | f), x, h);
-    }
-    static __device__ __forceinline__ void put(unsigned long long *p, unsigned a, float h)
-    {
-        st_word(p, ((unsigned long long)a << 32) | __float_as_uint(h));
+        st_word(p, ((unsigned long long)__float_as_uint(a) << 32) | __float_as_uint(h));
     }
     __device__ __forceinline__ void load(const unsigned long long *p) { w[0] = ld_word(p); }
     __device__ __forceinline__ bool there() const { return (unsigned)(w[0] >> 32) != 0xffffffffu; }
-    __device__ __forceinline__ float of(float x) const { return apply((unsigned)(w[0] >> 32), x, __uint_as_float((unsigned)w[0])); }
+    __device__ __forceinline__ float of(float x) const
+    {
+        return fma_of(__uint_as_float((unsigned)(w[0] >> 32)), x, __uint_as_float((unsigned)w[0]));
+    }
     static __device__ __forceinline__ unsigned inc_bits(float x) { return x == x ? __float_as_uint(x) : 0x7fffffffu; }
     static __device__ __forceinline__ float inc_value(unsigned v) { return __uint_as_float(v); }
     static __device__ __forceinline__ bool inc_there(unsigned v) { return v != 0xffffffffu; }
@@ -261,16 +246,12 @@ template <>
 struct Words<double> {
     static constexpr int N = 2;
     using Inc = unsigned long long;
-    using Map = double;
-    static __device__ __forceinline__ bool fixed(double a) { return is_const(a); }
     static constexpr unsigned long long NONE = ~0ull, QUIET = 0x7ff8000000000000ull;
     unsigned long long w[2];
     static __device__ __forceinline__ unsigned long long bits(double x)
     {
         return x == x ? (unsigned long long)__double_as_longlong(x) : QUIET;
     }
-    static __device__ __forceinline__ double pack(double a) { return a; }
-    static __device__ __forceinline__ double apply(double a, double x, double h) { return sla::apply(a, x, h); }
     static __device__ __forceinline__ void put(unsigned long long *p, double a, double h)
     {
         st_word(p, bits(a));
@@ -284,7 +265,7 @@ struct Words<double> {
     __device__ __forceinline__ bool there() const { return w[0] != NONE && w[1] != NONE; }
     __device__ __forceinline__ double of(double x) const
     {
-        return apply(__longlong_as_double((long long)w[0]), x, __longlong_as_double((long long)w[1]));
+        return fma_of(__longlong_as_double((long long)w[0]), x, __longlong_as_double((long long)w[1]));
     }
     static __device__ __forceinline__ unsigned long long inc_bits(double x) { return bits(x); }
     static __device__ __forceinline__ double inc_value(unsigned long long v) { return __longlong_as_double((long long)v); }
@@ -402,8 +383,7 @@ struct RecurSmem {
     unsigned long long full[P::N1S], late[P::NX];
     // per run and channel (A, H); then the map of the runs in front of it
     A mapA[P::NB][P::NR][P::W], mapH[P::NB][P::NR][P::W];
-    typename Words<A>::Map tileA[P::NB][P::W];     // the tile's map as published
-    A tileH[P::NB][P::W];
+    A tileA[P::NB][P::W], tileH[P::NB][P::W];      // the tile's map as published
     A enter[P::NB][P::W];                          // the state that enters the tile
     unsigned char fronts[P::NB][P::W];             // how the runs' maps are composed
     int begin[P::NP][P::C], finish[P::NP][P::C];   // sequence the scan enters / leaves at a position, or -1
@@ -1007,21 +987,21 @@ struct Recur {
         if (HELD == P::NR)
             take(buf, place, 0, q);
         tile_map(buf, place, q, ta, th);
-        typename Wd::Map pa = Wd::pack(pl.cut ? const_mark<A>() : add_of(ta, A(0)));
+        A pa = pl.cut ? const_mark<A>() : add_of(ta, A(0));
         int how = pl.cut ? 2 : 1;
         if (!(isfinite(ta) && isfinite(th)) && ch < g.n_chan) {
             how = 0;                                       // there is no map, a state warp goes through the rows
             if (pl.cut)
                 th = last_state(sm, buf, place);
             if (!(pl.cut && isfinite(th)))
-                pa = Wd::pack(A(0));
+                pa = A(0);
         }
         sm.fronts[buf][place] = (unsigned char)how;
         sm.tileA[buf][place] = pa;
         sm.tileH[buf][place] = th;
         if (pl.chunk + 1 < g.n_chunks && ch < g.n_chan) {
             const int64_t cell = (int64_t)pl.chunk * g.n_chan + ch;
-            if (Wd::fixed(pa))
+            if (is_const(pa))
                 st_word((typename Wd::Inc *)g.inc + cell, Wd::inc_bits(th));
             else if (how && enters(pl))
                 Wd::put(g.agg + cell * Wd::N, pa, th);
@@ -1032,7 +1012,7 @@ struct Recur {
     __device__ __forceinline__ void own_state(const TilePlan &pl, int slot, int buf, int place)
     {
         using Wd = Words<A>;
-        if (Wd::fixed(sm.tileA[buf][place]))                   // it is published
+        if (is_const(sm.tileA[buf][place]))                   // it is published
             return;
         bool own;
         const A x = walk<false>(g, sm, slot, buf, place, A(0), own);
@@ -1072,13 +1052,13 @@ struct Recur {
     {
         using Wd = Words<A>;
         const int64_t ch = (int64_t)pl.cb * P::W + chan_at(place);
-        const typename Wd::Map pa = sm.tileA[buf][place];
+        const A pa = sm.tileA[buf][place];
         const A th = sm.tileH[buf][place];
         sm.enter[buf][place] = x;
         if (ch >= g.n_chan)
             return;
-        bool own = Wd::fixed(pa);                              // published by the map warp
-        x = sm.fronts[buf][place] ? Wd::apply(pa, x, th) : walk<true>(g, sm, slot, buf, place, x, own);
+        bool own = is_const(pa);                              // published by the map warp
+        x = sm.fronts[buf][place] ? apply(pa, x, th) : walk<true>(g, sm, slot, buf, place, x, own);
         if (pl.chunk + 1 < g.n_chunks && !own)
             st_word((typename Wd::Inc *)g.inc + (int64_t)pl.chunk * g.n_chan + ch, Wd::inc_bits(x));
     }

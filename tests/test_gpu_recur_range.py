@@ -143,3 +143,28 @@ def test_products_beyond_the_range(kind, off):
                                              seq_off=ro, dh_last=put(first[::-1].copy(), ref.wide(kind)))
         assert np.array_equal(ref.host(db)[:, ok], lam[:, ok]) and np.array_equal(ref.host(got0)[:, ok], dh0[:, ok])
         assert (ref.host(da)[:, ok] == 0).all()
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_coefficients_close_to_one_over_many_tiles(back):
+    """A state of 1 over a thousand coefficients of 1 - 3 * 2^-24, one a tile, and ones: products and sums are exact
+    but for the coefficients' own, u = 2^-24 relative each, and one more where a tile's rows get their states.  Products
+    held in fewer than 24 bits lose up to 3 u a tile."""
+    rows, n, d, u = (160 if back else 176), 1000, 8, 2.0 ** -24
+    c = 1 - 3 * u
+    a = torch.ones(n * rows, d)
+    at = torch.arange(n) * rows + 5
+    a[n * rows - 1 - at if back else at] = c
+    zero = torch.zeros(n * rows, d, device="cuda")
+    used = np.zeros(n * rows)
+    used[at.numpy()] = 1
+    k = np.cumsum(used)
+    one = torch.ones(1, d, device="cuda")
+    if back:
+        _, got, end = sla.sla_recur_adjoint(a.cuda(), zero, None, h0=one, dh_last=one)
+        got, k = got.flip(0), k - used                     # lambda is in front of its row's coefficient
+    else:
+        got, end = sla.sla_recur_solve(a.cuda(), zero, one)
+    want = np.exp(k * np.log1p(-3 * u))[:, None] * np.ones((1, d))
+    ref.within(got, want, (k[:, None] + 2) * u * want)
+    ref.within(end, want[-1:], (n + 2) * u * want[-1:])
