@@ -557,7 +557,9 @@ struct Recur {
             }
         }
     }
-    // Wait for what load() started.  A barrier that never ended is marked in `lost`, and the rows come out as NaN.
+    // Wait for what load() started.  A barrier that never ended is marked in `lost`, and from then on the rows of this
+    // thread's runs come out as NaN: pass 1 hands over a map that is not finite, pass 2 starts from NaN and spoils the
+    // inputs that it reads, so that no first state behind a border makes finite rows of them either.
     __device__ __forceinline__ void loaded(int j)
     {
         lost = !mbar_wait(&sm.full[j % P::N1S], j / P::N1S & 1) || lost;
@@ -566,6 +568,18 @@ struct Recur {
     {
         if constexpr (P::NIN > 2)
             lost = !mbar_wait(&sm.late[j % P::NX], j / P::NX & 1) || lost;
+    }
+    // The thread's own rows: all bits set, a NaN in every type.
+    __device__ __forceinline__ void spoil(int st, int sx)
+    {
+        const uint4 x = make_uint4(~0u, ~0u, ~0u, ~0u);
+#pragma unroll 1
+        for (int i = 0; i < R; ++i) {
+            const int at = stage_row(p0 + i) * 8 + l8;
+            rows_of<1>(st)[at] = x;
+            if constexpr (P::NIN > 2)
+                rows_of<2>(sx)[at] = x;
+        }
     }
     template <int K>
     __device__ __forceinline__ void staged(int st, int i, A (&x)[V]) const
@@ -840,6 +854,10 @@ struct Recur {
 #pragma unroll
         for (int v = 0; v < V; ++v)
             x[v] = apply(a[v], x[v], h[v]);
+        if (lost) {
+            vset(x, A(NAN));
+            spoil(st, sx);
+        }
         if (pl.seg)
             pass2_rows<true>(pl, slot, st, sx, kp, x);
         else
