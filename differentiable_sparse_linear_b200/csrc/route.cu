@@ -807,6 +807,7 @@ sla_status sla_route_sort(int64_t n_tokens, int32_t top_k, int32_t n_experts, in
             SLA_TRY(allow(k_route_rank<I, false>, smem));
             k_route_rank<I, false><<<grid, 32 * warps, smem, s>>>(n, per, IT, n_experts, align, ids, n_slots, d_offsets,
                                                                  d_counts, d_entry, d_slot, (int32_t *)d_work);
+            SLA_CUDA_TRY(cudaGetLastError());              // the second launch takes the ranks as places to write to
             const size_t smem2 = sizeof(int) * (4 * (size_t)n_experts + 2 + SORTED);
             SLA_TRY(allow(k_route_place<I>, smem2));
             k_route_place<I><<<grid, ST, smem2, s>>>(n, per, n_experts, align, ids, n_slots, d_offsets, d_counts,
