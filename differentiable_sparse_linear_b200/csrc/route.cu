@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "seq_rows.cuh"
@@ -262,6 +263,23 @@ __global__ void __launch_bounds__(ST)
     }
     write_plan(n_experts, align, n_slots, cnt, off, blockIdx.x, gridDim.x, offsets, counts, entry);
 }
+
+// Lets a kernel have the shared memory of the largest call, once per device.  The limit belongs to the process, and calls may
+// be made at the same time: one that set its own size could lower another's between that one's set and its launch.
+template <auto KERNEL>
+static sla_status allow_smem(size_t most)
+{
+    static std::atomic<uint64_t> ready{0};                 // devices whose limit is set
+    int dev = 0;
+    SLA_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        SLA_CUDA_TRY(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most));
+        if (dev < 64)
+            ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    return SLA_SUCCESS;
+}
+static inline size_t place_smem(int n_experts) { return sizeof(int) * (4 * (size_t)n_experts + 2 + SORTED); }
 
 // Blocks of the two-launch sort: a tile each at least, at most 148, and histograms of 64 Ki numbers at most,
 // since every block of the second launch reads them all.
@@ -787,31 +805,25 @@ sla_status sla_route_sort(int64_t n_tokens, int32_t top_k, int32_t n_experts, in
     const int warps = sort_warps(n_experts);
     const int64_t blocks = sort_blocks(n, n_experts);
     const size_t smem = sort_smem(n_experts, warps, blocks == 1 && n > 1024);
-    auto allow = [&](auto kernel, size_t bytes) -> sla_status {
-        if (bytes > 48 << 10)
-            SLA_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
-        return SLA_SUCCESS;
-    };
     auto run = [&](auto ids) -> sla_status {
         using I = std::remove_const_t<std::remove_pointer_t<decltype(ids)>>;
         if (blocks == 1) {
             // few entries: a lane takes one, as long as there are warps
             const int w = (int)std::min<int64_t>(warps, std::max<int64_t>({1, (n + 31) / 32, ((int64_t)n_experts + 31) / 32}));
             const int turns = (int)std::max<int64_t>(1, (n + 32 * w - 1) / (32 * w));
-            SLA_TRY(allow(k_route_rank<I, true>, smem));
+            SLA_TRY((allow_smem<k_route_rank<I, true>>(sort_smem(MAX_EXPERTS, sort_warps(MAX_EXPERTS), true))));
             k_route_rank<I, true><<<1, 32 * w, smem, s>>>(n, n, turns, n_experts, align, ids, n_slots, d_offsets, d_counts,
                                                          d_entry, d_slot, nullptr);
         } else {
             const int64_t tile = (int64_t)warps * 32 * IT, per = ((n + blocks - 1) / blocks + tile - 1) / tile * tile;
             const unsigned grid = (unsigned)((n + per - 1) / per);
-            SLA_TRY(allow(k_route_rank<I, false>, smem));
+            SLA_TRY((allow_smem<k_route_rank<I, false>>(sort_smem(MAX_EXPERTS, sort_warps(MAX_EXPERTS), false))));
+            SLA_TRY(allow_smem<k_route_place<I>>(place_smem(MAX_EXPERTS)));
             k_route_rank<I, false><<<grid, 32 * warps, smem, s>>>(n, per, IT, n_experts, align, ids, n_slots, d_offsets,
                                                                  d_counts, d_entry, d_slot, (int32_t *)d_work);
             SLA_CUDA_TRY(cudaGetLastError());              // the second launch takes the ranks as places to write to
-            const size_t smem2 = sizeof(int) * (4 * (size_t)n_experts + 2 + SORTED);
-            SLA_TRY(allow(k_route_place<I>, smem2));
-            k_route_place<I><<<grid, ST, smem2, s>>>(n, per, n_experts, align, ids, n_slots, d_offsets, d_counts,
-                                                     d_entry, d_slot, (const int32_t *)d_work);
+            k_route_place<I><<<grid, ST, place_smem(n_experts), s>>>(n, per, n_experts, align, ids, n_slots, d_offsets, d_counts,
+                                                                     d_entry, d_slot, (const int32_t *)d_work);
         }
         SLA_CUDA_TRY(cudaGetLastError());
         return SLA_SUCCESS;

@@ -259,3 +259,41 @@ def test_rows_beyond_32_bit_offsets():
     want = sla.sla_route_dispatch(x, r, w)
     assert torch.equal(view, want)
     assert torch.equal(sla.sla_route_combine(view, r, w), sla.sla_route_combine(want, r, w))
+
+
+def test_sorts_from_several_host_threads():
+    """Calls of different expert counts at the same time through the C ABI, which releases the interpreter's lock: a call
+    changes nothing that another one's launch needs."""
+    import threading
+
+    from differentiable_sparse_linear_b200 import _lib
+    lib = _lib.load()
+    wrong, start = [], threading.Barrier(4)
+
+    def work(experts, top_k, seed):
+        stream = torch.cuda.Stream()
+        ids = choices(6000, top_k, experts, seed=seed, repeat=True)
+        n = ids.size
+        want = ref.sort(ids, experts, 1, n)
+        with torch.cuda.stream(stream):
+            d = torch.from_numpy(ids).cuda()
+            out = [torch.empty(s, dtype=torch.int32, device="cuda") for s in (experts + 1, experts, n, n)]
+            size = lib.sla_route_workspace_bytes(6000, top_k, experts)
+            mem = torch.empty(max(size, 1), dtype=torch.uint8, device="cuda")
+            stream.synchronize()
+            start.wait()
+            for _ in range(4000):
+                s = lib.sla_route_sort(6000, top_k, experts, 1, d.data_ptr(), 8, n, *[t.data_ptr() for t in out], mem.data_ptr(),
+                                       size, stream.cuda_stream)
+                if s:
+                    wrong.append((experts, s, lib.sla_last_error()))
+                    return
+            stream.synchronize()
+            if not all(np.array_equal(t.cpu().numpy(), w.reshape(-1)) for t, w in zip(out, want)):
+                wrong.append((experts, "result"))
+    threads = [threading.Thread(target=work, args=a) for a in ((4096, 2, 1), (1000, 2, 2), (4096, 1, 3), (700, 1, 4))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
