@@ -1038,11 +1038,11 @@ struct Recur {
     __device__ __forceinline__ void own_state(const TilePlan &pl, int slot, int buf, int place)
     {
         using Wd = Words<A>;
-        if (is_const(sm.tileA[buf][place]))                   // it is published
+        if (pl.chunk + 1 == g.n_chunks || is_const(sm.tileA[buf][place]))   // nobody asks, or it is published
             return;
         bool own;
         const A x = walk<false>(g, sm, slot, buf, place, A(0), own);
-        if (own && pl.chunk + 1 < g.n_chunks)
+        if (own)
             st_word((typename Wd::Inc *)g.inc + (int64_t)pl.chunk * g.n_chan + (int64_t)pl.cb * P::W + chan_at(place), Wd::inc_bits(x));
     }
 
@@ -1062,9 +1062,10 @@ struct Recur {
             return g.enter ? g.enter[(int64_t)pl.first * g.n_chan + ch] : A(0);
         if (!enters(pl))
             return A(0);
-        // A look waits longer the more words it loads: four chunks where about as many are at work at a time (16384 x
-        // 4096 bf16, 64 channel tiles: 106 us, with eight 113, with 16 160), eight where it is more (32768 x 2560, 40
-        // tiles: 132 us, with four and then 16 163), 16 where it is far more (40000 x 304, 5 tiles: 56 us, with eight 60).
+        // A look waits longer the more words it loads, and loads as many as chunks may be at work (gridDim.x / n_cb): four
+        // up to 2.5 of them, eight up to 12, 16 above.  Measured at 2.3 (16384 x 4096 bf16, 64 channel tiles: four 106 us, eight
+        // 113, 16 160), 3.7 (32768 x 2560, 40 tiles: eight 132, four 163) and 30 (40000 x 304, 5 tiles: 16 56, eight 60); the
+        // borders lie between these.
         const typename Words<A>::Inc *inc = (const typename Words<A>::Inc *)g.inc;
         const int n = (int)gridDim.x;
         if (g.n_cb * 5 >= n * 2)

@@ -41,6 +41,30 @@ def test_rows_without_alignment_give_the_aligned_bits(kind, gate, d):
             assert all(torch.equal(p, q) for p, q in zip(got, want))
 
 
+# rows of a tile: forward, backward, backward with the sigmoid gate
+TILES = (176, 160, 144)
+
+
+@pytest.mark.parametrize("rows", TILES)
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f64"])
+@pytest.mark.parametrize("gate", sla.GATES)
+def test_ends_and_borders_at_tile_ends(rows, kind, gate):
+    """Totals of a tile, two and three, one row more or less, and borders there, counted from either end (backward
+    tiles are counted from the last row)."""
+    kind = ref.KINDS[kind]
+    for tokens, off in ([(n * rows + k, [0, n * rows + k]) for n in (1, 2) for k in (-1, 0, 1)] +
+                        [(3 * rows + k, [0, rows + m, 2 * rows + m, 3 * rows + k]) for k in (0, 5) for m in (-1, 0, 1)] +
+                        [(3 * rows + 5, [0, rows + m + 5, 2 * rows + m + 5, 3 * rows + 5]) for m in (-1, 0, 1)] +
+                        [(3 * rows, [rows, rows, 2 * rows, 2 * rows]), (3 * rows, [rows - 1, rows, 2 * rows, 2 * rows + 1])]):
+        for d in (40, 33):
+            x = data((tokens, off), d, kind, gate)
+            h, last = sla.sla_recur_solve(x["a"], x["b"], x["h0"], x["off"], gate=gate)
+            check_solve(x, h, last, gate, kind)
+            got = sla.sla_recur_adjoint(x["a"], h, x["dh"], b=x["b"], h0=x["h0"], seq_off=x["off"], dh_last=x["dlast"],
+                                        gate=gate)
+            check_adjoint(x, h, got, gate, kind)
+
+
 @pytest.mark.parametrize("gate,kind", [("value", "f32"), ("value", "f64"), ("sigmoid", "f32"), ("exp", "bf16")])
 @pytest.mark.parametrize("back", [False, True])
 def test_long_memory(gate, kind, back):
