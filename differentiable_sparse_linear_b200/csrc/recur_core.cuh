@@ -626,18 +626,16 @@ struct Recur {
     struct Kept {
         A k[R][V];
     };
-    template <int N>
-    static __device__ __forceinline__ void keep(A (&k)[N], const A (&a)[N], const A (&w)[N])
+    static __device__ __forceinline__ void keep(A (&k)[V], const A (&a)[V], const A (&w)[V])
     {
 #pragma unroll
-        for (int v = 0; v < N; ++v)
+        for (int v = 0; v < V; ++v)
             k[v] = GATE != SLA_GATE_SIGMOID || a[v] <= w[v] ? a[v] : -w[v];
     }
-    template <int N>
-    static __device__ __forceinline__ void kept(const A (&k)[N], A (&a)[N], A (&w)[N])
+    static __device__ __forceinline__ void kept(const A (&k)[V], A (&a)[V], A (&w)[V])
     {
 #pragma unroll
-        for (int v = 0; v < N; ++v) {
+        for (int v = 0; v < V; ++v) {
             if constexpr (GATE == SLA_GATE_SIGMOID) {
                 const bool other = signbit(k[v]);
                 const A rest = add_of(A(1), other ? k[v] : -k[v]);
@@ -671,8 +669,6 @@ struct Recur {
             A a[V], w[V], y[V];
             gates_of<GATE, sizeof(S) == 2>(z, a, w);
             keep(kp.k[i], a, w);
-            if constexpr (GATE == SLA_GATE_SIGMOID)        // the coefficients of pass 2: near 1 they are 1 - w, rounded once
-                kept(kp.k[i], a, w);
             if (SEG && s >= 0) {                           // a sequence begins
                 get_states(g.enter, s, c0 + l8 * V, mh);
                 cut = true;
@@ -968,12 +964,8 @@ struct Recur {
             }
             A a[N], w[N];
             gates_of<GATE, sizeof(S) == 2>(z, a, w);
-            if constexpr (GATE == SLA_GATE_SIGMOID) {
-                keep(z, a, w);
-                kept(z, a, w);
-                if constexpr (!REV)
-                    vmul(u, w, u);
-            }
+            if constexpr (!REV && GATE == SLA_GATE_SIGMOID)
+                vmul(u, w, u);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int p = p0 + i;

@@ -207,8 +207,10 @@ __device__ __forceinline__ double rcp_of(double x) { return 1.0 / x; }
 // truncation at |z| = 1/4 is 2^-26 and whose error is the rounding of the last sum.
 //
 // sigmoid: both halves come from one e = exp(-z), a = 1 / (1 + e) and w = e a, so that 1 - a keeps its digits where
-// a rounds to 1.  z is held above -86 (fp64: -700), where e would leave the range and a is below 1e-37
-// anyway.  An error of e counts 1 - a times in a, so the plain exp2 is enough for 16-bit rows.
+// a rounds to 1, and the larger a is 1 - w, rounded once: the approximate reciprocal's errors have one sign, and a
+// state carried over ten thousand rows collected them (2700 units of 2^-24, 620 so).  z is held above -86 (fp64: -700),
+// where e would leave the range and a is below 1e-37 anyway.  An error of e counts 1 - a times in a, so the plain
+// exp2 is enough for 16-bit rows.
 template <int GATE, bool FAST, typename A, int N>
 __device__ __forceinline__ void gates_of(const A (&z)[N], A (&a)[N], A (&w)[N])
 {
@@ -267,6 +269,9 @@ __device__ __forceinline__ void gates_of(const A (&z)[N], A (&a)[N], A (&w)[N])
         for (int i = 0; i < N; ++i)
             a[i] = rcp_of(a[i]);
         vmul(w, e, a);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            a[i] = a[i] <= w[i] ? a[i] : add_of(A(1), -w[i]);
     }
 }
 

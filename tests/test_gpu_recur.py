@@ -491,3 +491,25 @@ def test_offsets_out_of_range_stay_inside():
         guard = torch.full((720, 16), 5.0, device="cuda")
         sla.sla_recur_solve(x["a"], x["b"], x["h0"], off, out=guard[10:710])
         assert (guard[:10] == 5).all() and (guard[710:] == 5).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_many_steps_of_a_slow_sigmoid_gate(kind):
+    """Ten thousand steps at coefficients about 0.9999, inputs of one sign.  Bound: a step rounds its coefficient (1 - w) and its
+    sum, u / 2 each below 1 (the sum relative to itself, u), and the weighted input 9 u; every error counts a times in
+    the next step.  All of one sign, that is E_t = a E_{t-1} + 1.5 u G_t, besides the inputs' 9 u G_t."""
+    kind, d, u = ref.KINDS[kind], 16, 2.0 ** -24
+    g = torch.Generator().manual_seed(4)
+    rows = 50
+    z = torch.log(1 / (2e-4 * torch.rand(rows, d, generator=g, dtype=torch.float64) + 1e-9) - 1).to(kind)
+    b = (torch.rand(rows, d, generator=g) + 0.5).to(kind)
+    state = torch.zeros(1, d, device="cuda")
+    v, err = np.zeros(d), np.zeros(d)
+    gz, gb = z.cuda(), b.cuda()
+    c, w = ref.gate_of(ref.host(z), "sigmoid")
+    for t in range(10000):
+        r = t % rows
+        sla.sla_recur_step(gz[r:r + 1], gb[r:r + 1], state, gate="sigmoid")
+        v = c[r] * v + w[r] * ref.host(b)[r]
+        err = c[r] * err + 1.5 * u * v
+    ref.within(state, v[None], ref.storage(v, err + 9 * u * v, torch.float32)[None])
