@@ -296,3 +296,21 @@ def test_routing_refuses(native):
             (lambda: sla.sla_route_combine_adjoint(x, r, x.bfloat16()), "ys must be")]:
         with pytest.raises(ValueError, match=words):
             call()
+
+
+def test_workspace_sizes(lib):
+    """A call of several tiles or blocks needs a workspace, and says so; one of a single tile does not."""
+    rows = dict(n_tokens=100000, n_chan=64, lda=64, ldb=64, ldh=64)
+    for dtype, width in ((0, 4), (1, 8), (2, 4), (3, 4)):
+        need = lib.sla_recur_workspace_bytes(dtype, 100000, 64)
+        assert need >= 100000 // 176 * 64 * 3 * width        # a map and a state a channel of every tile
+        assert lib.sla_recur_solve(*solve_args(dtype=dtype, work=P, bytes=need - 1, **rows)) == INVALID
+        assert lib.sla_recur_solve(*solve_args(dtype=dtype, work=None, bytes=need, **rows)) == INVALID
+        assert lib.sla_recur_solve(*solve_args(dtype=dtype, work=P + 8, bytes=need, **rows)) == INVALID
+        assert lib.sla_recur_workspace_bytes(dtype, 144, 64) == 0
+    need = lib.sla_route_workspace_bytes(100000, 8, 256)
+    assert need >= 2 * 256 * 4                             # a histogram a block
+    a = [100000, 8, 256, 1, P, 4, 800000, P, P, P, P]
+    assert lib.sla_route_sort(*a, P, need - 1, None) == INVALID
+    assert lib.sla_route_sort(*a, None, need, None) == INVALID
+    assert lib.sla_route_workspace_bytes(1000, 8, 256) == 0
