@@ -1355,8 +1355,6 @@ __global__ void __launch_bounds__(RecurShape<S, GATE, REV>::NT, 1) k_recur(const
 }
 
 // ------------------------------------------------------------------ launch
-int sm_count();
-
 template <typename S, int GATE, int U, bool REV>
 sla_status launch_recur_u(RecurArgs<S> &g, cudaStream_t s)
 {

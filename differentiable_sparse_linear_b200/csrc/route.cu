@@ -281,8 +281,9 @@ static sla_status allow_smem(size_t most)
 }
 static inline size_t place_smem(int n_experts) { return sizeof(int) * (4 * (size_t)n_experts + 2 + SORTED); }
 
-// Blocks of the two-launch sort: a tile each at least, at most 148, and histograms of 64 Ki numbers at most,
-// since every block of the second launch reads them all.
+// Blocks of the two-launch sort: a tile each at least, at most 148 (a B200's SMs; a constant, for the workspace's size is
+// asked without a device), and histograms of 64 Ki numbers at most, since every block of the second launch reads
+// them all.
 static inline int64_t sort_blocks(int64_t n, int n_experts)
 {
     const int64_t tile = (int64_t)sort_warps(n_experts) * 32 * IT;
@@ -674,7 +675,7 @@ static inline int group_of(int64_t n_tokens, int64_t n_chan, int U, int NV)
         int G = 32;
         while (G < PT && (int64_t)G * NV * turns < nunits)
             G *= 2;
-        if (turns == 1 || n_tokens * G >= 148 * 2048)
+        if (turns == 1 || n_tokens * G >= (int64_t)sm_count() * 2048)
             return G;
     }
 }
@@ -687,7 +688,7 @@ sla_status launch_product(RouteArgs<S> &g, bool to_slots, cudaStream_t s)
     if (to_slots) {
         // a fill block for every 64 KiB of slot rows that may be blank, at most two an SM
         const int64_t bytes = g.n_slots * g.n_chan * (int64_t)sizeof(S);
-        g.fill_blocks = (int)std::max<int64_t>(1, std::min<int64_t>(296, bytes >> 16));
+        g.fill_blocks = (int)std::max<int64_t>(1, std::min<int64_t>(2 * sm_count(), bytes >> 16));
         k_route_to_slots<S, U, KU, NV, DW><<<(unsigned)(blocks + g.fill_blocks), PT, 0, s>>>(g, G);
     } else if (blocks > 0)
         k_route_to_tokens<S, U, KU, NV, DW><<<(unsigned)blocks, PT, 0, s>>>(g, G);

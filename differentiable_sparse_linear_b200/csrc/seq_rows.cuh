@@ -55,6 +55,9 @@ static inline sla_status with_row_type(int32_t dtype, F f)
 static inline bool row_dtype_ok(int32_t dtype) { return dtype >= SLA_F32 && dtype <= SLA_F16; }
 static inline size_t row_bytes(int32_t dtype) { return dtype == SLA_F64 ? 8 : dtype == SLA_F32 ? 4 : 2; }
 
+// SMs of the current device (recur.cu)
+int sm_count();
+
 // sums and products that are never contracted, so that every variant of a loop rounds alike
 __device__ __forceinline__ float add_of(float a, float b) { return __fadd_rn(a, b); }
 __device__ __forceinline__ double add_of(double a, double b) { return __dadd_rn(a, b); }
