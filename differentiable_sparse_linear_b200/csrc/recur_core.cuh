@@ -37,17 +37,17 @@
 // is bounded all the same, and a chunk that gave up goes on with NaN.
 //
 // What bounds it.  Memory must carry z, b and h once (backward z, g, h, dz, db): 6 (10) bytes a value in 16
-// bits.  The kernel moves little more (380 of 403 MB at 16384 x 4096 bf16, forward, besides 8 + 4 bytes a channel
-// and chunk of published words) but runs at 0.55 to 0.6 of the copy rate there, 105 us, 0.66 in fp32 (16384 x
-// 2048, 93 us), backward 0.6 (170 us) and 0.79 (130 us): about 23 instructions a value at 39 % of the issue
-// slots.  Warps wait for one another's results once a tile and for fixed latencies in between; 16 warps of 128
-// registers are all that fit. Measured on the way (solve 65536 x 4096 bf16): every gate twice instead of kept
-// coefficients and combining runs by shuffles 655 us, maps by the scan warps 532, four scan threads a channel 501,
-// tensor copies, kept coefficients and paired arithmetic 455, first states as entering states 424, guards out of
-// line 403 to 414.  Rows of 128 bytes by a bulk copy each took 185 us where tensor copies take 105 (16384 x 4096);
-// copies by one warp's cp.async 171; runs of 8 rows by 7 warps 157; two blocks of half a tile an SM 215.  Few
-// channels leave few chunks side by side and the chain of chunks bounds: 200000 x 64 bf16 takes 106 us of a floor
-// of 12.  Tiles with borders cost half as much again (16384 x 4096 in 100 sequences: 161 us).
+// bits.  The kernel moves little more (376 of 403 MB at 16384 x 4096 bf16, forward, besides 8 + 4 bytes a channel
+// and chunk of published words) but runs at 0.59 of the copy rate there, 103 us, 0.65 to 0.69 in fp32 (16384 x 2048, 89 to
+// 95 us), backward 0.70 (146 us) and 0.75 (136 us): about 23 instructions a value at 43 % of the issue slots.
+// Warps wait for one another's results once a tile and for fixed latencies in between; 16 warps of 128 registers are
+// all that fit.  Measured on the way (solve 65536 x 4096 bf16): every gate twice instead of kept coefficients and
+// combining runs by shuffles 655 us, maps by the scan warps 532, four scan threads a channel 501, tensor copies, kept
+// coefficients and paired arithmetic 455, first states as entering states 424, guards out of line 403 to 414, maps
+// published as they are 362 to 385.  Rows of 128 bytes by a bulk copy each took 185 us where tensor copies took 105 (16384 x
+// 4096); copies by one warp's cp.async 171; runs of 8 rows by 7 warps 157; two blocks of half a tile an SM 215.  Few
+// channels leave few chunks side by side and the chain of chunks bounds: 200000 x 64 bf16 takes 75 us of a floor
+// of 12.  Tiles with borders cost half as much again (16384 x 4096 in 100 sequences: 155 us).
 //
 // A sequence border inside a run makes its map constant.  Such a map is marked by A = -0 (products are
 // normalised to +0), because 0 * x would carry a NaN or an infinity across the border.
@@ -55,7 +55,8 @@
 // A channel whose (A, H) is not finite has no map: a coefficient or an input is not, or a product or a sum of the
 // tile left the range, although the states themselves may stay in it.  Its rows are read again and taken one
 // by one from the state that enters the tile, and later chunks wait for the one that leaves.  A product that
-// vanishes counts as 0.
+// vanishes counts as 0.  Rows full of NaN need no wait: solve 65536 x 4096 bf16 820 us; coefficients of 2 over
+// rows of zeros, whose every tile overflows, take 13.5 ms there.
 #pragma once
 
 #include <cuda.h>
@@ -1399,8 +1400,8 @@ bool box_map(CUtensorMap *map, const S *p, int64_t n_tokens, int64_t n_chan, int
 
 // By alignment: tensor copies where every array's rows are aligned to 16 bytes and every input has a stride (a row
 // expanded over the tokens has none); else units of 4 bytes (two of a 16-bit type) or one value.  Copies
-// below 4 bytes are not asynchronous.  16384 rows of 1000, 1002 and 1001 bf16: 54, 71 and 132 us; of 1024 and 1001
-// fp32: 58 and 91 us.
+// below 4 bytes are not asynchronous.  16384 rows of 1000, 1002 and 1001 bf16: 46, 71 and 128 us; of 1024 and 1001
+// fp32: 54 and 91 us; one row of coefficients expanded over 16384 x 4096 bf16 177 us, as many full ones 97.
 template <typename S, int GATE, bool REV>
 sla_status launch_recur(RecurArgs<S> &g, cudaStream_t s)
 {

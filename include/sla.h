@@ -362,7 +362,8 @@ SLA_API sla_status sla_pcg_solve_batched_noalloc(const sla_csr *A, const sla_pre
  *   - Rows are [n_tokens][n_chan], channels contiguous, with a row stride `ld*` in elements
  *     (ld >= n_chan; an input's ld may be 0, one row for every token).  Values are SLA_F32,
  *     SLA_F64, SLA_BF16 or SLA_F16; arithmetic, states, weights and their gradients are fp32
- *     (fp64 with SLA_F64 rows), and every row value is rounded once, when it is written.
+ *     (fp64 with SLA_F64 rows), and every row value is rounded once, when it is written.  Gates
+ *     are functions with an error of a few units of that type (16-bit rows: 2^-22 relative).
  *     Row pointers need the alignment of their type only.
  *   - Packed sequences: sequence s owns rows [d_seq_off[s], d_seq_off[s+1]) of the packed rows
  *     (device int32, n_seq + 1 entries, ascending, within [0, n_tokens]; empty sequences
