@@ -392,15 +392,18 @@ SLA_API size_t sla_recur_workspace_bytes(int32_t dtype, int64_t n_tokens, int64_
 /* h_t = a_t h_{t-1} + w_t b_t over every sequence, from d_h0 (n_seq x n_chan, fp32 or fp64;
  * NULL: zero states).  d_h gets
  * the rows; d_h_last (n_seq x n_chan, fp32/fp64, may be NULL) the unrounded last states (an empty
- * sequence's is its first one).  flags: 0 or SLA_FILL_REST.  A state that is not finite is not to
- * the end of its sequence (it may turn from infinite to NaN), and reaches no other channel or
- * sequence.  A coefficient that is not finite makes it so whatever the state in front of it, 0 and a
- * sequence's missing first state included (0 times it is NaN).  Finite coefficients over several
- * rows may have a product beyond the range where the states stay inside: the result is that of one
- * row after the other, but such rows are slow.  A product of coefficients of consecutive rows below
- * 2^-126 (fp64: 2^-1022) in magnitude may count as 0: what is left of the state in front of them is
- * lost then, also where later coefficients above 1 would bring it back.  The adjoint's lambda has
- * the same limits. */
+ * sequence's is its first one).  flags: 0 or SLA_FILL_REST.
+ *
+ * What is not finite: behind an input or first state that is not, a state is not to the end of its
+ * sequence (it may turn from infinite to NaN), and it reaches no other channel or sequence.  A
+ * coefficient that is not finite makes it so whatever the state in front of it, 0 and a sequence's
+ * missing first state included (0 times it is NaN).  What leaves the range: a state beyond it is
+ * infinite, and may be finite again where later coefficients bring its value back.  Where only a
+ * product of coefficients over several rows is beyond it and the states are not, the result is
+ * that of one row after the other, but such rows are slow.  A product of coefficients of consecutive
+ * rows below 2^-126 (fp64: 2^-1022) in magnitude may count as 0: what is left of the state in front
+ * of them is lost then, also where later coefficients above 1 would bring it back.  All of this
+ * holds for the adjoint's lambda as well. */
 SLA_API sla_status sla_recur_solve(int32_t dtype, int32_t gate, int64_t n_tokens, int64_t n_chan,
                                    int32_t n_seq, const int32_t *d_seq_off, const void *d_a,
                                    int64_t lda, const void *d_b, int64_t ldb, const void *d_h0,
