@@ -394,10 +394,10 @@ SLA_API size_t sla_recur_workspace_bytes(int32_t dtype, int64_t n_tokens, int64_
  * the rows; d_h_last (n_seq x n_chan, fp32/fp64, may be NULL) the unrounded last states (an empty
  * sequence's is its first one).  flags: 0 or SLA_FILL_REST.
  *
- * What is not finite: behind an input or first state that is not, a state is not to the end of its
- * sequence (it may turn from infinite to NaN), and it reaches no other channel or sequence.  A
- * coefficient that is not finite makes it so whatever the state in front of it, 0 and a sequence's
- * missing first state included (0 times it is NaN).  What leaves the range: a state beyond it is
+ * Infinities and NaN: from an input or first state that is not finite on, no state of its channel is
+ * to the end of its sequence (it may turn from infinite to NaN); other channels and sequences do not
+ * see it.  The same goes for a coefficient that is not finite, whatever the state in front of it, 0
+ * and a sequence's missing first state included (0 times it is NaN).  Range: a state beyond it is
  * infinite, and may be finite again where later coefficients bring its value back.  Where only a
  * product of coefficients over several rows is beyond it and the states are not, the result is
  * that of one row after the other, but such rows are slow.  A product of coefficients of consecutive
